@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import itertools
 import os
-from typing import Optional, Sequence, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import numpy as np
 import torch
@@ -41,12 +41,18 @@ DLC_N_BUCKETS = 256
 DLC_ALIGN_ELEMS = 64
 DLC_RANGE_FIELDS = 4
 DLC_STATIC_SCRATCH_BYTES = 64 << 20
+DLC_FLOAT32 = 0
+DLC_BFLOAT16 = 1
+DLC_FLOAT16 = 2
+DLC_MAX_GROUPS = 16
+DLC_CODE_BLOCK = 64
 
 EXPORTED = (
     "dlc_fragment_plan", "dlc_workspace_bytes", "dlc_quantize_range", "dlc_quantize_encode",
     "dlc_quantize", "dlc_quantize_static", "dlc_quantize_bases", "dlc_merge_outer_step", "dlc_merge_weights", "dlc_broadcast",
     "dlc_cycle_workspace_bytes", "dlc_outer_cycle", "dlc_outer_cycle_lanes", "dlc_ring_workspace_bytes", "dlc_ring_outer_step",
     "dlc_rda_workspace_bytes", "dlc_rda_outer_step", "dlc_cycle_rda_workspace_bytes", "dlc_outer_cycle_rda",
+    "dlc_grad_norm_workspace_bytes", "dlc_grad_norm", "dlc_adamw_step", "dlc_adamw_coded_step",
     "dlc_last_error", "dlc_version",
 )
 
@@ -63,6 +69,19 @@ class NoQuorumError(DlcError):
 
 class _Tensor(ctypes.Structure):
     _fields_ = [("offset", ctypes.c_int64), ("loffset", ctypes.c_int64), ("numel", ctypes.c_int64)]
+
+
+class AdamWGroup(NamedTuple):
+    """Hyperparameters of the tensors of one group (dlc_adamw_step)."""
+    lr: float = 1e-3
+    beta1: float = 0.9
+    beta2: float = 0.999
+    eps: float = 1e-8
+    weight_decay: float = 0.01
+
+
+class _Group(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_double) for name in AdamWGroup._fields]
 
 
 def _load() -> ctypes.CDLL:
@@ -97,6 +116,12 @@ def _load() -> ctypes.CDLL:
         "dlc_cycle_rda_workspace_bytes": [i32, tp, vp, i32, ctypes.POINTER(sz)],
         "dlc_outer_cycle_rda": [vp, vp, vp, i64, i32, vp, tp, vp, i32, vp, vp, vp, vp, ctypes.c_double,
                                 ctypes.c_double, u32, vp, sz, vp, i32],
+        "dlc_grad_norm_workspace_bytes": [i32, tp, i32, ctypes.POINTER(sz)],
+        "dlc_grad_norm": [vp, i32, i64, i32, vp, tp, i32, ctypes.c_double, ctypes.c_double, vp, vp, vp, sz, vp],
+        "dlc_adamw_step": [vp, vp, i32, vp, vp, vp, i64, i32, vp, tp, i32, vp, ctypes.POINTER(_Group), i32, vp, vp,
+                           vp, i32, vp],
+        "dlc_adamw_coded_step": [vp, vp, i32, vp, vp, vp, vp, vp, i64, i32, vp, tp, i32, vp, ctypes.POINTER(_Group),
+                                 i32, ctypes.c_uint64, vp, vp, vp, i32, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -120,9 +145,23 @@ def _check(rc: int) -> None:
         raise DlcError(rc, msg)
 
 
+class TensorList(tuple):
+    """A list of (offset, loffset, numel) triples converted once: every call takes it
+    as its `tensors`, with nothing left to convert (a training loop passes the same
+    list at every step)."""
+
+    def __new__(cls, tensors: Sequence[Tuple[int, int, int]]):
+        self = super().__new__(cls, tensors)
+        self._c = _tensors(tuple(self))
+        self._ends = _extents(tuple(self))
+        return self
+
+
 def _tensors(tensors: Sequence[Tuple[int, int, int]]):
     """dlc_tensor array of (offset, loffset, numel) triples: one int64 [n][3] array
     viewed as the C structs (the ctypes array keeps that buffer alive)."""
+    if isinstance(tensors, TensorList):
+        return tensors._c
     n = len(tensors)
     if n == 0:
         return (_Tensor * 1)(), 0
@@ -202,6 +241,8 @@ class _Checks:
 
 def _extents(tensors) -> Tuple[int, int]:
     """(end of the last tensor in theta_global, end of the last in a learner row)."""
+    if isinstance(tensors, TensorList):
+        return tensors._ends
     if len(tensors) == 0:
         return 0, 0
     return max(int(o) + int(n) for o, _, n in tensors), max(int(lo) + int(n) for _, lo, n in tensors)
@@ -580,3 +621,167 @@ def outputs_for(n_learners: int, learner_stride: int, n_tensors: int, device="cu
     codebook = torch.empty((n_learners, n_tensors, DLC_N_BUCKETS), dtype=torch.float32, device=device)
     rng = torch.empty((n_learners, n_tensors, DLC_RANGE_FIELDS), dtype=torch.float32, device=device)
     return codes, codebook, rng
+
+
+# ---------------------------------------------------------------------------
+# The learners' inner step
+# ---------------------------------------------------------------------------
+_FLOAT_TYPES = {torch.float32: DLC_FLOAT32, torch.bfloat16: DLC_BFLOAT16, torch.float16: DLC_FLOAT16}
+
+
+def _float_type(t, name: str, types) -> int:
+    """The C ABI's number of t's element type."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
+    if t.dtype not in types:
+        raise ValueError(f"{name} must be one of {', '.join(map(str, types))}, not {t.dtype}")
+    return _FLOAT_TYPES[t.dtype]
+
+
+def _per_learner(c: _Checks, t, name: str, k: int, dtype: torch.dtype):
+    c.need(t, name, dtype)
+    if tuple(t.shape) != (k,):
+        raise ValueError(f"{name} must have shape ({k},), not {tuple(t.shape)}")
+
+
+class _OnDevice:
+    """The buffers' device made current for the call where it is not, and the stream
+    on it: the caller's, or that device's current one."""
+
+    def __init__(self, device: torch.device, stream):
+        if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the call's buffers on {device}")
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self.stream = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def group_ids(group_of: Sequence[int]) -> np.ndarray:
+    """Group of each tensor as the C ABI reads it (a training loop converts it once)."""
+    return np.ascontiguousarray(group_of, dtype=np.int32)
+
+
+def dlc_grad_norm_workspace_bytes(n_learners: int, tensors) -> int:
+    arr, n = _tensors(tensors)
+    out = ctypes.c_size_t(0)
+    _check(_lib.dlc_grad_norm_workspace_bytes(int(n_learners), arr, n, ctypes.byref(out)))
+    return out.value
+
+
+def alloc_grad_norm_workspace(n_learners: int, tensors, device="cuda") -> torch.Tensor:
+    nbytes = max(256, dlc_grad_norm_workspace_bytes(n_learners, tensors))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def dlc_grad_norm(grads, tensors, norm, grad_scale, workspace, max_norm=float("inf"), unscale=1.0, present=None,
+                  stream=None):
+    """Every present learner's gradient norm, times `unscale`, into norm, and the factor
+    that unscales and clips its gradients into grad_scale (0 where the norm is not
+    finite); both device fp64 [K].  grads: [K, learner_stride] fp32, bf16 or fp16."""
+    gt = _float_type(grads, "grads", tuple(_FLOAT_TYPES))
+    if grads.dim() != 2:
+        raise ValueError("grads must be a [K, learner_stride] tensor")
+    k, stride = grads.shape
+    _present_list(present, k)
+    c = _Checks()
+    c.need(grads, "grads", grads.dtype)
+    if _extents(tensors)[1] > stride:
+        raise ValueError(f"a tensor reaches past learner_stride {stride}")
+    _per_learner(c, norm, "norm", k, torch.float64)
+    _per_learner(c, grad_scale, "grad_scale", k, torch.float64)
+    c.workspace(workspace)
+    c.done()
+    arr, n = _tensors(tensors)
+    _buf, pres = _present(present, k)
+    with _OnDevice(grads.device, stream) as s:
+        _check(_lib.dlc_grad_norm(_ptr(grads), gt, stride, k, pres, arr, n, float(unscale), float(max_norm),
+                                  _ptr(norm), _ptr(grad_scale), _ptr(workspace), workspace.numel(), s))
+
+
+def coded_moments(n_learners: int, learner_stride: int, device="cuda"):
+    """Zero moments for dlc_adamw_coded_step: (m codes, m scales, v codes, v scales).  The
+    value of a code is code.float() * 2^(scale - 127), scale that of its 64 elements."""
+    blocks = learner_stride // DLC_CODE_BLOCK
+    out = []
+    for dtype in (torch.float8_e4m3fn, torch.float8_e5m2):
+        out.append(torch.zeros((n_learners, learner_stride), dtype=torch.uint8, device=device).view(dtype))
+        out.append(torch.zeros((n_learners, blocks), dtype=torch.uint8, device=device))
+    return tuple(out)
+
+
+def _adamw(theta_L, grads, moments, steps, tensors, groups, group_of, grad_scale, lr_scale, working, present):
+    """Buffer checks of an AdamW call -> the arguments its two forms share.  moments:
+    (name, tensor, dtype, row length as a fraction of the learner's) each."""
+    c = _Checks()
+    k, stride = c.learners(theta_L, tensors)
+    _present_list(present, k)
+    gt = _float_type(grads, "grads", tuple(_FLOAT_TYPES))
+    c.rows(grads, "grads", k, stride, grads.dtype)
+    for name, t, dtype, per in moments:
+        c.rows(t, name, k, stride // per, dtype)
+    _per_learner(c, steps, "steps", k, torch.int64)
+    if grad_scale is not None:
+        _per_learner(c, grad_scale, "grad_scale", k, torch.float64)
+    if lr_scale is not None:
+        _per_learner(c, lr_scale, "lr_scale", k, torch.float64)
+    wt = DLC_FLOAT32
+    if working is not None:
+        wt = _float_type(working, "working", (torch.bfloat16, torch.float16))
+        c.rows(working, "working", k, stride, working.dtype)
+    if isinstance(groups, AdamWGroup):
+        groups = (groups,)
+    gs = (_Group * max(1, len(groups)))(*[tuple(g) for g in groups])
+    ids = None
+    if group_of is not None:
+        ids = group_ids(group_of)
+        if ids.shape != (len(tensors),):
+            raise ValueError(f"group_of holds {ids.size} values for {len(tensors)} tensors")
+    c.done()
+    arr, n = _tensors(tensors)
+    buf, pres = _present(present, k)
+    keep = (buf, ids)  # alive until the call returns
+    return (gt, stride, k, pres, arr, n, None if ids is None else ctypes.c_void_p(ids.ctypes.data), gs, len(groups),
+            _ptr(grad_scale), _ptr(lr_scale), _ptr(working), wt, keep)
+
+
+def dlc_adamw_step(theta_L, grads, exp_avg, exp_avg_sq, steps, tensors, groups=AdamWGroup(), group_of=None,
+                   grad_scale=None, lr_scale=None, working=None, present=None, stream=None):
+    """One AdamW step of every present learner, in place: theta_L, exp_avg and exp_avg_sq
+    fp32 [K, learner_stride], grads the same in fp32, bf16 or fp16, steps int64 [K]
+    (counted up).  groups: an AdamWGroup or a list of them, with group_of naming each
+    tensor's; grad_scale, lr_scale: device fp64 [K] (a learner whose grad_scale is not
+    finite and positive is left out); working: bf16 or fp16 [K, learner_stride], the
+    updated parameters rounded."""
+    gt, stride, k, pres, arr, n, ids, gs, ng, scale, lrs, work, wt, _keep = _adamw(
+        theta_L, grads, (("exp_avg", exp_avg, torch.float32, 1), ("exp_avg_sq", exp_avg_sq, torch.float32, 1)), steps,
+        tensors, groups, group_of, grad_scale, lr_scale, working, present)
+    with _OnDevice(theta_L.device, stream) as s:
+        _check(_lib.dlc_adamw_step(_ptr(theta_L), _ptr(grads), gt, _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(steps),
+                                   stride, k, pres, arr, n, ids, gs, ng, scale, lrs, work, wt, s))
+
+
+def dlc_adamw_coded_step(theta_L, grads, m_codes, m_scales, v_codes, v_scales, steps, tensors, groups=AdamWGroup(),
+                         group_of=None, seed=0, grad_scale=None, lr_scale=None, working=None, present=None,
+                         stream=None):
+    """dlc_adamw_step with the moments in 8 bits (coded_moments allocates them): m_codes
+    float8_e4m3fn and v_codes float8_e5m2 [K, learner_stride], m_scales and v_scales uint8
+    [K, learner_stride / 64].  seed: of the stochastic rounding, 0 <= seed < 2^64."""
+    if not 0 <= int(seed) < 1 << 64:
+        raise ValueError("seed must be in [0, 2^64)")
+    gt, stride, k, pres, arr, n, ids, gs, ng, scale, lrs, work, wt, _keep = _adamw(
+        theta_L, grads,
+        (("m_codes", m_codes, torch.float8_e4m3fn, 1), ("m_scales", m_scales, torch.uint8, DLC_CODE_BLOCK),
+         ("v_codes", v_codes, torch.float8_e5m2, 1), ("v_scales", v_scales, torch.uint8, DLC_CODE_BLOCK)),
+        steps, tensors, groups, group_of, grad_scale, lr_scale, working, present)
+    with _OnDevice(theta_L.device, stream) as s:
+        _check(_lib.dlc_adamw_coded_step(_ptr(theta_L), _ptr(grads), gt, _ptr(m_codes), _ptr(m_scales),
+                                         _ptr(v_codes), _ptr(v_scales), _ptr(steps), stride, k, pres, arr, n, ids, gs,
+                                         ng, int(seed), scale, lrs, work, wt, s))

@@ -5,7 +5,7 @@
 
 (run as a script: importing the package needs the library that this script compiles)
 
-Each source compiles to an object under _build/ (the two in parallel), then the
+Each source compiles to an object under _build/ (in parallel), then the
 objects link into the library.  libdlc_hostsan.so is the same library with its
 host code (argument checks, fragment plans, block partitions, workspace layouts,
 launch orchestration) built with AddressSanitizer and UndefinedBehaviorSanitizer;
@@ -26,7 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdlc.so")
 LIB_HOSTSAN = os.path.join(PKG, "libdlc_hostsan.so")
-SOURCES = ["dlc_api.hip", "dlc_kernels.hip"]
+SOURCES = ["dlc_api.hip", "dlc_kernels.hip", "dlc_inner.hip"]  # the C ABI, then the kernels
 ARCH = "gfx950"
 
 FLAGS = [
@@ -97,9 +97,10 @@ def build(verbose: bool = False, hostsan: bool = True) -> str:
         jobs.append(("dlc_api.hip", os.path.join(OBJ, "dlc_api_hostsan.o"), HOSTSAN))
     with ThreadPoolExecutor(len(jobs)) as ex:
         objs = list(ex.map(lambda j: _compile(*j, verbose), jobs))
-    _link(objs[:2], LIB, verbose)
+    n = len(SOURCES)
+    _link(objs[:n], LIB, verbose)
     if hostsan:
-        _link([objs[2], objs[1]], LIB_HOSTSAN, verbose, sanitize=True)
+        _link([objs[n], *objs[1:n]], LIB_HOSTSAN, verbose, sanitize=True)
     return LIB
 
 

@@ -1,0 +1,85 @@
+// Launch descriptors of the learner's inner step (gradient norm, AdamW), shared by
+// the host orchestration and the gfx950 kernels.
+//
+// These calls work on learner rows only.  An element's arithmetic depends on its
+// tensor through the tensor's group alone, so the host joins tensors of one group
+// that follow each other without padding into one range, and a launch carries up
+// to kMaxRanges ranges in its kernel arguments.  Within a launch each range owns a
+// contiguous run of blocks (grid x); the present learners are grid y.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace dlc {
+
+constexpr int kMaxRanges = 236;
+constexpr int kMaxGroups = 16;
+constexpr int kInnerBlock = 256;                      // threads per block
+constexpr int kInnerTile = 4096;                      // elements per tile
+constexpr int kCodeBlock = 64;                        // elements that share a scale byte
+
+enum FloatType : int32_t { kF32 = 0, kBF16 = 1, kF16 = 2, kNone = -1 };
+
+struct InnerRange {
+  uint32_t lo64;         // first element of the row, in units of 64
+  uint32_t count;        // elements
+  uint32_t block_first;  // first block of this range within the launch
+};
+
+struct InnerGeom {
+  int32_t n_ranges;
+  int32_t n_blocks;
+  int32_t tiles_per_block;
+  int32_t slot_base;     // the launch's first slot of block partials
+  InnerRange r[kMaxRanges];
+  uint8_t group[kMaxRanges];
+};
+
+struct InnerGroup {
+  double lr, beta1, beta2, eps, weight_decay;
+};
+
+struct AdamWArgs {
+  float* theta;               // [n_learners][stride]
+  const void* grads;          // [n_learners][stride]
+  void* m;                    // fp32, or e4m3 codes
+  void* v;                    // fp32, or e5m2 codes
+  uint8_t* m_scale;           // [n_learners][stride / 64] (coded moments)
+  uint8_t* v_scale;
+  void* working;              // 16-bit copy of theta, or NULL
+  int64_t* steps;             // [n_learners]
+  const double* grad_scale;   // [n_learners], or NULL
+  const double* lr_scale;     // [n_learners], or NULL
+  int64_t stride;
+  uint64_t seed;
+  int32_t n_present;
+  uint8_t learner[64];        // present position -> learner
+  InnerGroup group[kMaxGroups];
+};
+
+struct NormArgs {
+  const void* grads;
+  int64_t stride;
+  double* part;               // [slot][n_present] sums of squares
+  double* norm;               // [n_learners]
+  double* grad_scale;         // [n_learners]
+  double unscale, max_norm;
+  int32_t n_present;
+  int32_t n_slots;
+  uint8_t learner[64];
+};
+
+// HIP passes at most 4 KB of kernel arguments.
+static_assert(sizeof(AdamWArgs) + sizeof(InnerGeom) <= 4096 && sizeof(NormArgs) + sizeof(InnerGeom) <= 4096);
+
+// Kernel launchers (dlc_inner.hip).  Each returns hipSuccess or the launch error.
+hipError_t launch_norm_partial(const NormArgs& a, int32_t grad_type, const InnerGeom& g, hipStream_t s);
+hipError_t launch_norm_final(const NormArgs& a, hipStream_t s);
+hipError_t launch_adamw(const AdamWArgs& a, int32_t grad_type, int32_t working_type, bool coded, const InnerGeom& g,
+                        hipStream_t s);
+// steps[i] += 1 for every present learner whose step was not left out
+hipError_t launch_adamw_advance(const AdamWArgs& a, hipStream_t s);
+
+}  // namespace dlc

@@ -83,6 +83,16 @@ extern "C" {
 #define DLC_ALIGN_ELEMS 64
 #define DLC_RANGE_FIELDS 4
 
+/* Element types of gradients and of the 16-bit working copy of the parameters. */
+#define DLC_FLOAT32 0
+#define DLC_BFLOAT16 1
+#define DLC_FLOAT16 2
+
+/* Hyperparameter groups of one dlc_adamw_step call. */
+#define DLC_MAX_GROUPS 16
+/* Consecutive elements that share a scale byte in dlc_adamw_coded_step. */
+#define DLC_CODE_BLOCK 64
+
 typedef struct dlc_tensor {
     int64_t offset;   /* element offset into theta_global and momentum        */
     int64_t loffset;  /* element offset into each learner row (theta, codes)  */
@@ -451,6 +461,120 @@ int32_t dlc_rda_outer_step(float* theta_global, float* momentum, const float* th
                            const double* weights, double lr, double beta, uint8_t* codes, float* codebook,
                            float* range, double* sq_norms, void* workspace, size_t workspace_bytes,
                            void* hip_stream);
+
+/*
+ * The learners' inner step (INTELLECT-1 notes, section 3.2 steps 2-3: between two
+ * outer steps every learner takes H AdamW steps on its own replica).  The calls
+ * below run one such step for every present learner of one device: the gradient
+ * norm with its clipping factor, then AdamW with 32-bit or with 8-bit moments.
+ * Gradients and moments are laid out like the learner rows ([n_learners] rows of
+ * learner_stride elements, tensor t at [loffset, loffset + numel); a tensor's
+ * `offset` is not used).  Only elements of the call's tensors in present learners'
+ * rows are read or written.  Nothing synchronizes, nothing is kept between calls
+ * but the caller's buffers, and results do not depend on how the tensors are
+ * ordered or split over launches: a call can be captured in a HIP graph and replayed.
+ */
+
+/*
+ * dlc_grad_norm -- every learner's global gradient norm and the factor its step
+ * multiplies its gradients with.  For every present learner i, over all tensors:
+ *   norm[i]       = unscale * sqrt(sum of grads^2)        (fp64, in a fixed order)
+ *   grad_scale[i] = unscale * min(1, max_norm / norm[i]), or 0 where norm[i] is not
+ *                   finite (dlc_adamw_step then leaves that learner's step out)
+ *   grads       device [n_learners][learner_stride] of grad_type (DLC_FLOAT32,
+ *               DLC_BFLOAT16 or DLC_FLOAT16), read only, 256-byte aligned
+ *   present     host uint8 [n_learners] (0 = absent: its entries stay untouched) or
+ *               NULL = all present; at least one present (else DLC_ERR_NO_QUORUM)
+ *   unscale     finite and > 0: the inverse of the loss scale and of the number of
+ *               accumulated micro-batches
+ *   max_norm    > 0; INFINITY = no clipping
+ *   norm, grad_scale  device fp64 [n_learners], written for present learners
+ *   workspace   >= dlc_grad_norm_workspace_bytes(n_learners, tensors, n_tensors)
+ *               bytes, 256-byte aligned, no initial contents required
+ * The sum's order depends on the tensor list alone: repeated calls agree bit for bit.
+ */
+int32_t dlc_grad_norm_workspace_bytes(int32_t n_learners, const dlc_tensor* tensors, int32_t n_tensors,
+                                      size_t* bytes);
+
+int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stride, int32_t n_learners,
+                      const uint8_t* present, const dlc_tensor* tensors, int32_t n_tensors, double unscale,
+                      double max_norm, double* norm, double* grad_scale, void* workspace, size_t workspace_bytes,
+                      void* hip_stream);
+
+/*
+ * dlc_adamw_step -- one AdamW step over all tensors of every present learner, with
+ * 32-bit moments (decoupled weight decay).  With t = steps[i] + 1, g = grad_scale[i]
+ * * grad and eta = lr * lr_scale[i], per element, in the tensor's group:
+ *   m     <- beta1 m + (1 - beta1) g
+ *   v     <- beta2 v + (1 - beta2) g^2
+ *   theta <- (1 - eta weight_decay) theta
+ *            - eta / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *   working <- theta rounded to working_type (nearest even)
+ *   steps[i] <- t
+ * m, v and theta are computed in fp64 and rounded to fp32 once; the quotient is an
+ * fp32 expression of the rounded moments, within 2^-20 of its value.
+ *   theta_learners  device fp32 [n_learners][learner_stride], updated in place
+ *   grads       as dlc_grad_norm
+ *   exp_avg     device fp32 [n_learners][learner_stride]: m (start with zeros)
+ *   exp_avg_sq  device fp32 [n_learners][learner_stride]: v, never negative
+ *   steps       device int64 [n_learners]: steps taken so far, counted up by the
+ *               call.  It belongs to the call's tensors: a model stepped in several
+ *               calls keeps one array for each.
+ *   groups      host [n_groups], 1..DLC_MAX_GROUPS; lr and weight_decay finite and
+ *               >= 0, betas in [0, 1), eps a normal positive fp32 number
+ *   group_of    host int32 [n_tensors]: group of each tensor; NULL = all group 0
+ *   grad_scale  device fp64 [n_learners], or NULL = 1.  A learner whose entry is not
+ *               finite and > 0 is left out: nothing of it is written, its step is
+ *               not counted.
+ *   lr_scale    device fp64 [n_learners], or NULL = 1: the schedule's factor, read
+ *               when the call runs (a replayed graph follows the schedule)
+ *   working     device [n_learners][learner_stride] of working_type (DLC_BFLOAT16 or
+ *               DLC_FLOAT16), or NULL (working_type is then ignored)
+ * The buffers must not overlap.  Device pointers 256-byte aligned, except steps,
+ * grad_scale and lr_scale: 8-byte aligned.
+ */
+typedef struct dlc_adamw_group {
+    double lr, beta1, beta2, eps, weight_decay;
+} dlc_adamw_group;
+
+int32_t dlc_adamw_step(float* theta_learners, const void* grads, int32_t grad_type, float* exp_avg,
+                       float* exp_avg_sq, int64_t* steps, int64_t learner_stride, int32_t n_learners,
+                       const uint8_t* present, const dlc_tensor* tensors, int32_t n_tensors, const int32_t* group_of,
+                       const dlc_adamw_group* groups, int32_t n_groups, const double* grad_scale,
+                       const double* lr_scale, void* working, int32_t working_type, void* hip_stream);
+
+/*
+ * dlc_adamw_coded_step -- the same step with the moments held in 8 bits: m as OCP
+ * e4m3 codes, v as OCP e5m2 codes, each block of DLC_CODE_BLOCK consecutive row
+ * elements with one scale byte s (e8m0): the value is code * 2^(s - 127).
+ * The new moments (fp64, rounded to fp32) step theta as above and are then coded.
+ * Per block, with E the biased exponent field of the largest finite fp32 magnitude
+ * among the block's elements that belong to a tensor:
+ *   s    = max(E - 7, 0) for m, max(E - 14, 0) for v
+ *   y    = |x| * 2^(127 - s)
+ *   code = sign and floor(y / u + (r + 1/2) / 2^16) * u, u the format's step at y
+ *          (below the smallest normal number, y is first rounded to a multiple of
+ *          2^-20 u for m and 2^-21 u for v)
+ * with r the low (m) or high (v) 16 bits of the element's random word
+ *   x0 = e + k1;  x1 = (x0 ^ x0 >> 16) * 0x9E3779B9 + k2;
+ *   x2 = (x1 ^ x1 >> 15) * 0x6A09E667;  word = x2 ^ x2 >> 16        (mod 2^32)
+ *   mix(x) = the same with k1 = k2 = 0
+ *   k1 = mix(mix(seed + t) + i + 64 * (e >> 32)),  k2 = mix(k1 + (seed >> 32) + t)
+ * of row element e, learner i and step t, so the coding error is zero on average
+ * and a call's results depend on its arguments alone.  A positive v is never coded
+ * as 0 (its code is at least 1), so no update divides by eps alone; a value that
+ * is not finite becomes NaN.
+ *   m_codes, v_codes    device uint8 [n_learners][learner_stride], all zeros at the start
+ *   m_scales, v_scales  device uint8 [n_learners][learner_stride / 64], likewise
+ * Other arguments, layout and errors as dlc_adamw_step.
+ */
+int32_t dlc_adamw_coded_step(float* theta_learners, const void* grads, int32_t grad_type, uint8_t* m_codes,
+                             uint8_t* m_scales, uint8_t* v_codes, uint8_t* v_scales, int64_t* steps,
+                             int64_t learner_stride, int32_t n_learners, const uint8_t* present,
+                             const dlc_tensor* tensors, int32_t n_tensors, const int32_t* group_of,
+                             const dlc_adamw_group* groups, int32_t n_groups, uint64_t seed,
+                             const double* grad_scale, const double* lr_scale, void* working, int32_t working_type,
+                             void* hip_stream);
 
 /* Message of the last error on the calling thread ("" if none). */
 const char* dlc_last_error(void);
