@@ -26,7 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdlc.so")
 LIB_HOSTSAN = os.path.join(PKG, "libdlc_hostsan.so")
-SOURCES = ["dlc_api.hip", "dlc_kernels.hip", "dlc_inner.hip"]  # the C ABI, then the kernels
+API_SOURCES = ["dlc_api.hip", "dlc_inner_api.hip"]  # host code only: sanitized in libdlc_hostsan.so
+SOURCES = [*API_SOURCES, "dlc_kernels.hip", "dlc_inner.hip"]
 ARCH = "gfx950"
 
 FLAGS = [
@@ -94,13 +95,13 @@ def build(verbose: bool = False, hostsan: bool = True) -> str:
     os.makedirs(OBJ, exist_ok=True)
     jobs = [(s, os.path.join(OBJ, s.replace(".hip", ".o")), []) for s in SOURCES]
     if hostsan:
-        jobs.append(("dlc_api.hip", os.path.join(OBJ, "dlc_api_hostsan.o"), HOSTSAN))
+        jobs += [(s, os.path.join(OBJ, s.replace(".hip", "_hostsan.o")), HOSTSAN) for s in API_SOURCES]
     with ThreadPoolExecutor(len(jobs)) as ex:
         objs = list(ex.map(lambda j: _compile(*j, verbose), jobs))
     n = len(SOURCES)
     _link(objs[:n], LIB, verbose)
     if hostsan:
-        _link([objs[n], *objs[1:n]], LIB_HOSTSAN, verbose, sanitize=True)
+        _link([*objs[n:], *objs[len(API_SOURCES):n]], LIB_HOSTSAN, verbose, sanitize=True)
     return LIB
 
 

@@ -4,11 +4,10 @@
 // Nothing here allocates device memory, keeps state between calls or waits on the
 // stream; argument errors are reported before anything is enqueued.
 #include "dlc.h"
-#include "dlc_inner.h"
+#include "dlc_host.h"
 #include "dlc_internal.h"
 
 #include <algorithm>
-#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -23,9 +22,12 @@
 // start zeroed: every workspace slot is written before it is read.
 static __device__ __align__(256) unsigned char scratch[DLC_STATIC_SCRATCH_BYTES];
 
+// Errors and argument checks, shared with the inner step's calls (dlc_host.h).
+namespace dlc {
 namespace {
-
 thread_local std::string g_last_error;
+constexpr int64_t kMaxOffset = (int64_t(1) << 38) - DLC_ALIGN_ELEMS;
+}  // namespace
 
 int32_t fail(int32_t code, const std::string& msg) {
   g_last_error = msg;
@@ -36,6 +38,64 @@ int32_t ok() {
   g_last_error.clear();
   return DLC_OK;
 }
+
+const char* last_error() { return g_last_error.c_str(); }
+
+int32_t out_of_memory() noexcept {
+  g_last_error = "out of memory";
+  return DLC_ERR_WORKSPACE;
+}
+
+int32_t hip_fail(hipError_t e, const char* what) {
+  return fail(DLC_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+int32_t check_tensors(const dlc_tensor* t, int32_t n, int64_t learner_stride, bool need_loffset) {
+  if (t == nullptr) return fail(DLC_ERR_INVALID_ARGUMENT, "tensors is NULL");
+  if (n < 1) return fail(DLC_ERR_INVALID_ARGUMENT, "n_tensors must be >= 1");
+  if (need_loffset && (learner_stride < 1 || learner_stride % DLC_ALIGN_ELEMS != 0))
+    return fail(DLC_ERR_ALIGNMENT, "learner_stride must be a positive multiple of 64 elements");
+  for (int32_t i = 0; i < n; ++i) {
+    const dlc_tensor& d = t[i];
+    if (d.numel < 1 || d.numel > kMaxTensorNumel)
+      return fail(DLC_ERR_INVALID_ARGUMENT, "tensor " + std::to_string(i) + ": numel must be in [1, 2^32 - 1]");
+    if (d.offset > kMaxOffset || d.loffset > kMaxOffset)
+      return fail(DLC_ERR_INVALID_ARGUMENT, "tensor " + std::to_string(i) + ": offset beyond 2^38 elements");
+    if (d.offset < 0 || d.loffset < 0)
+      return fail(DLC_ERR_INVALID_ARGUMENT, "tensor " + std::to_string(i) + ": negative offset");
+    if (d.offset % DLC_ALIGN_ELEMS != 0 || d.loffset % DLC_ALIGN_ELEMS != 0)
+      return fail(DLC_ERR_ALIGNMENT, "tensor " + std::to_string(i) + ": offset and loffset must be multiples of 64 elements");
+    if (need_loffset && d.loffset + d.numel > learner_stride)
+      return fail(DLC_ERR_INVALID_ARGUMENT, "tensor " + std::to_string(i) + ": loffset + numel exceeds learner_stride");
+  }
+  // No two tensors may overlap in theta_global, nor within a learner row.
+  std::vector<int32_t> order(n);
+  for (int pass = 0; pass < 2; ++pass) {
+    std::iota(order.begin(), order.end(), 0);
+    auto key = [&](int32_t i) { return pass == 0 ? t[i].offset : t[i].loffset; };
+    const auto before = [&](int32_t x, int32_t y) { return key(x) < key(y); };
+    // lists are nearly always in row order already
+    if (!std::is_sorted(order.begin(), order.end(), before)) std::sort(order.begin(), order.end(), before);
+    for (int32_t i = 1; i < n; ++i) {
+      if (key(order[i - 1]) + t[order[i - 1]].numel > key(order[i]))
+        return fail(DLC_ERR_INVALID_ARGUMENT, std::string("tensors ") + std::to_string(order[i - 1]) + " and " +
+                                                  std::to_string(order[i]) + " overlap in " +
+                                                  (pass == 0 ? "theta_global" : "the learner rows"));
+    }
+  }
+  return DLC_OK;
+}
+
+}  // namespace dlc
+
+using dlc::aligned256;
+using dlc::check_tensors;
+using dlc::fail;
+using dlc::hip_fail;
+using dlc::ok;
+using dlc::round256;
+
+namespace {
 
 // Blocks per call that the statistics, encode and send-back passes aim for
 // (several resident blocks per CU on 256 CUs).  Finer blocks shorten the tail at
@@ -58,11 +118,6 @@ constexpr int64_t kBroadcastBlocks = 8192;
 // already get bigger blocks from the targets above.
 constexpr int64_t kStatsMinTiles = 4;
 constexpr int64_t kEncodeMinTiles = 4;
-
-constexpr int64_t kMaxTensorNumel = (int64_t(1) << 32) - 1;
-constexpr int64_t kMaxOffset = (int64_t(1) << 38) - DLC_ALIGN_ELEMS;
-
-bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
 struct Partition {
   std::vector<dlc::LaunchGeom> launches;
@@ -148,8 +203,6 @@ struct WorkspaceLayout {
   size_t stats = 0, hist = 0, hist_sum = 0, status = 0, total = 0;
 };
 
-size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
-
 // Workspace: per-block statistics partials, per-block packed histograms, then
 // the histogram slice entries (at most slots / kHistSlice + tensors + 2).
 WorkspaceLayout workspace_layout(int64_t stats_slots, int64_t hist_slots, int32_t n_tensors, int32_t n_learners) {
@@ -161,42 +214,6 @@ WorkspaceLayout workspace_layout(int64_t stats_slots, int64_t hist_slots, int32_
   w.status = w.hist_sum + round256(entries * (size_t)n_learners * dlc::kBuckets * 2 * sizeof(uint64_t));
   w.total = w.status + 256;  // one status word (debug checks), padded
   return w;
-}
-
-int32_t check_tensors(const dlc_tensor* t, int32_t n, int64_t learner_stride, bool need_loffset) {
-  if (t == nullptr) return fail(DLC_ERR_INVALID_ARGUMENT, "tensors is NULL");
-  if (n < 1) return fail(DLC_ERR_INVALID_ARGUMENT, "n_tensors must be >= 1");
-  if (need_loffset && (learner_stride < 1 || learner_stride % DLC_ALIGN_ELEMS != 0))
-    return fail(DLC_ERR_ALIGNMENT, "learner_stride must be a positive multiple of 64 elements");
-  for (int32_t i = 0; i < n; ++i) {
-    const dlc_tensor& d = t[i];
-    if (d.numel < 1 || d.numel > kMaxTensorNumel)
-      return fail(DLC_ERR_INVALID_ARGUMENT, "tensor " + std::to_string(i) + ": numel must be in [1, 2^32 - 1]");
-    if (d.offset > kMaxOffset || d.loffset > kMaxOffset)
-      return fail(DLC_ERR_INVALID_ARGUMENT, "tensor " + std::to_string(i) + ": offset beyond 2^38 elements");
-    if (d.offset < 0 || d.loffset < 0)
-      return fail(DLC_ERR_INVALID_ARGUMENT, "tensor " + std::to_string(i) + ": negative offset");
-    if (d.offset % DLC_ALIGN_ELEMS != 0 || d.loffset % DLC_ALIGN_ELEMS != 0)
-      return fail(DLC_ERR_ALIGNMENT, "tensor " + std::to_string(i) + ": offset and loffset must be multiples of 64 elements");
-    if (need_loffset && d.loffset + d.numel > learner_stride)
-      return fail(DLC_ERR_INVALID_ARGUMENT, "tensor " + std::to_string(i) + ": loffset + numel exceeds learner_stride");
-  }
-  // No two tensors may overlap in theta_global, nor within a learner row.
-  std::vector<int32_t> order(n);
-  for (int pass = 0; pass < 2; ++pass) {
-    std::iota(order.begin(), order.end(), 0);
-    auto key = [&](int32_t i) { return pass == 0 ? t[i].offset : t[i].loffset; };
-    const auto before = [&](int32_t x, int32_t y) { return key(x) < key(y); };
-    // lists are nearly always in row order already
-    if (!std::is_sorted(order.begin(), order.end(), before)) std::sort(order.begin(), order.end(), before);
-    for (int32_t i = 1; i < n; ++i) {
-      if (key(order[i - 1]) + t[order[i - 1]].numel > key(order[i]))
-        return fail(DLC_ERR_INVALID_ARGUMENT, std::string("tensors ") + std::to_string(order[i - 1]) + " and " +
-                                                  std::to_string(order[i]) + " overlap in " +
-                                                  (pass == 0 ? "theta_global" : "the learner rows"));
-    }
-  }
-  return DLC_OK;
 }
 
 struct Common {
@@ -247,10 +264,6 @@ int32_t setup_quant(Common& c, const float* theta_global, const float* theta_lea
   c.status = reinterpret_cast<uint32_t*>(ws + wl.status);
   c.stream = static_cast<hipStream_t>(hip_stream);
   return DLC_OK;
-}
-
-int32_t hip_fail(hipError_t e, const char* what) {
-  return fail(DLC_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
 }
 
 int32_t run_range(Common& c) {
@@ -527,7 +540,7 @@ int32_t outer_cycle(float* theta_global, float* momentum, float* theta_learners,
     lane[f] = lanes ? busy++ % n_lanes : 0;
     const double* w = weights + (size_t)f * n_learners;
     rc = prepare_merge(margs[f], theta_global, momentum, codes, learner_stride, n_learners, codebook, w, lr, beta);
-    if (rc != DLC_OK) return fail(rc, "fragment " + std::to_string(f) + ": " + g_last_error);
+    if (rc != DLC_OK) return fail(rc, "fragment " + std::to_string(f) + ": " + dlc::last_error());
     for (int32_t i = 0; i < n_learners; ++i) present[i] = w[i] > 0.0 ? 1 : 0;
     void* lane_ws = workspace == nullptr ? nullptr : static_cast<char*>(workspace) + (size_t)lane[f] * share;
     size_t quant_bytes = share;
@@ -541,7 +554,7 @@ int32_t outer_cycle(float* theta_global, float* momentum, float* theta_learners,
     rc = setup_quant(qc[f], theta_global, theta_learners, learner_stride, n_learners, present.data(),
                      tensors + fragment_first[f], n, lane_ws, quant_bytes,
                      lanes ? lane_streams[lane[f]] : quantize_stream, fragment_first[f], n_tensors);
-    if (rc != DLC_OK) return fail(rc, "fragment " + std::to_string(f) + ": " + g_last_error);
+    if (rc != DLC_OK) return fail(rc, "fragment " + std::to_string(f) + ": " + dlc::last_error());
     qc[f].args.range = reinterpret_cast<float4*>(range);
     qc[f].args.codes = codes;
     qc[f].args.codebook = codebook;
@@ -727,181 +740,6 @@ int32_t static_scratch(int dev, void** ptr) {
     return fail(DLC_ERR_HIP, "static scratch address is not 256-byte aligned");
   *ptr = g_scratch_ptr[dev];
   return DLC_OK;
-}
-
-// ---------------------------------------------------------------------------
-// The learners' inner step: gradient norm, AdamW.
-// ---------------------------------------------------------------------------
-constexpr int64_t kNormBlocks = 2048;
-constexpr int64_t kAdamWTiles = 2;
-
-struct InnerPartition {
-  std::vector<dlc::InnerGeom> launches;
-  int64_t n_slots = 0;
-};
-
-// Tensors of one group that follow each other in the row without padding become one
-// range (of at most 2^32 - 1 elements); every range gets ceil(tiles / tiles_per_block)
-// blocks, tiles_per_block at least min_tiles and such that the call has about
-// target_blocks blocks.
-InnerPartition inner_partition(const dlc_tensor* t, int32_t n, const int32_t* group_of, int64_t min_tiles,
-                               int64_t target_blocks) {
-  struct Range {
-    int64_t lo, count;
-    int32_t group;
-  };
-  std::vector<Range> ranges;
-  ranges.reserve(n);
-  for (int32_t i = 0; i < n; ++i) {
-    const int32_t group = group_of ? group_of[i] : 0;
-    if (!ranges.empty()) {
-      Range& b = ranges.back();
-      if (b.group == group && b.lo + b.count == t[i].loffset && b.count + t[i].numel <= kMaxTensorNumel) {
-        b.count += t[i].numel;
-        continue;
-      }
-    }
-    ranges.push_back({t[i].loffset, t[i].numel, group});
-  }
-  int64_t tiles = 0;
-  for (const Range& r : ranges) tiles += (r.count + dlc::kInnerTile - 1) / dlc::kInnerTile;
-  const int64_t tpb = std::max(min_tiles, (tiles + target_blocks - 1) / target_blocks);
-  InnerPartition p;
-  for (size_t s = 0; s < ranges.size(); s += dlc::kMaxRanges) {
-    dlc::InnerGeom g;
-    std::memset(&g, 0, sizeof(g));
-    g.n_ranges = (int32_t)std::min<size_t>(dlc::kMaxRanges, ranges.size() - s);
-    g.tiles_per_block = (int32_t)tpb;
-    g.slot_base = (int32_t)p.n_slots;
-    int64_t blocks = 0;
-    for (int32_t i = 0; i < g.n_ranges; ++i) {
-      const Range& r = ranges[s + i];
-      g.r[i] = {(uint32_t)(r.lo / DLC_ALIGN_ELEMS), (uint32_t)r.count, (uint32_t)blocks};
-      g.group[i] = (uint8_t)r.group;
-      blocks += (r.count + tpb * dlc::kInnerTile - 1) / (tpb * dlc::kInnerTile);
-    }
-    g.n_blocks = (int32_t)blocks;
-    p.n_slots += blocks;
-    p.launches.push_back(g);
-  }
-  return p;
-}
-
-InnerPartition norm_partition(const dlc_tensor* t, int32_t n) { return inner_partition(t, n, nullptr, 1, kNormBlocks); }
-
-// A grid's x extent times its block must stay below 2^32 threads.
-constexpr int64_t kAdamWMaxBlocks = int64_t(1) << 22;
-
-InnerPartition adamw_partition(const dlc_tensor* t, int32_t n, const int32_t* group_of) {
-  return inner_partition(t, n, group_of, kAdamWTiles, kAdamWMaxBlocks);
-}
-
-bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
-
-// The present learners' indices -> list, their number; 0 = an error was set.
-int32_t present_learners(int32_t n_learners, const uint8_t* present, uint8_t* list, int32_t* rc) {
-  *rc = DLC_OK;
-  if (n_learners < 1 || n_learners > DLC_MAX_LEARNERS) {
-    *rc = fail(DLC_ERR_INVALID_ARGUMENT, "n_learners must be in [1, 64]");
-    return 0;
-  }
-  int32_t kp = 0;
-  for (int32_t i = 0; i < n_learners; ++i) {
-    if (present == nullptr || present[i] != 0) list[kp++] = (uint8_t)i;
-  }
-  if (kp == 0) *rc = fail(DLC_ERR_NO_QUORUM, "no learner is present");
-  return kp;
-}
-
-int32_t check_float_type(int32_t type, const char* name, bool wide) {
-  if (type == DLC_BFLOAT16 || type == DLC_FLOAT16 || (wide && type == DLC_FLOAT32)) return DLC_OK;
-  return fail(DLC_ERR_INVALID_ARGUMENT, std::string(name) + " is not one of the call's types");
-}
-
-// No C++ exception crosses the ABI: running out of host memory is an error code (the
-// message fits a string's own storage).
-template <typename F>
-int32_t no_throw(F&& f) noexcept {
-  try {
-    return f();
-  } catch (...) {
-    g_last_error = "out of memory";
-    return DLC_ERR_WORKSPACE;
-  }
-}
-
-// The moments of an AdamW call: 32-bit, or codes and scale bytes.
-struct Moments {
-  void* m;
-  void* v;
-  uint8_t* m_scales;
-  uint8_t* v_scales;
-  bool coded;
-  uint64_t seed;
-};
-
-int32_t adamw_step(float* theta_learners, const void* grads, int32_t grad_type, const Moments& mo, int64_t* steps,
-                   int64_t learner_stride, int32_t n_learners, const uint8_t* present, const dlc_tensor* tensors,
-                   int32_t n_tensors, const int32_t* group_of, const dlc_adamw_group* groups, int32_t n_groups,
-                   const double* grad_scale, const double* lr_scale, void* working, int32_t working_type,
-                   void* hip_stream) {
-  dlc::AdamWArgs a;
-  std::memset(&a, 0, sizeof(a));
-  int32_t rc;
-  a.n_present = present_learners(n_learners, present, a.learner, &rc);
-  if (rc != DLC_OK) return rc;
-  if (!theta_learners || !grads || !mo.m || !mo.v || !steps || (mo.coded && (!mo.m_scales || !mo.v_scales)))
-    return fail(DLC_ERR_INVALID_ARGUMENT, "theta_learners, grads, the moments and steps must not be NULL");
-  const void* buffers[] = {theta_learners, grads, mo.m, mo.v, mo.m_scales, mo.v_scales, working};
-  for (const void* p : buffers) {
-    if (!aligned256(p)) return fail(DLC_ERR_ALIGNMENT, "device pointers must be 256-byte aligned");
-    if (p && std::count(std::begin(buffers), std::end(buffers), p) > 1)
-      return fail(DLC_ERR_INVALID_ARGUMENT, "the call's buffers must not overlap");
-  }
-  if (!aligned8(steps) || !aligned8(grad_scale) || !aligned8(lr_scale))
-    return fail(DLC_ERR_ALIGNMENT, "steps, grad_scale and lr_scale must be 8-byte aligned");
-  rc = check_float_type(grad_type, "grad_type", true);
-  if (rc == DLC_OK && working) rc = check_float_type(working_type, "working_type", false);
-  if (rc == DLC_OK) rc = check_tensors(tensors, n_tensors, learner_stride, true);
-  if (rc != DLC_OK) return rc;
-  if (!groups || n_groups < 1 || n_groups > DLC_MAX_GROUPS)
-    return fail(DLC_ERR_INVALID_ARGUMENT, "groups must hold 1 to 16 groups");
-  for (int32_t q = 0; q < n_groups; ++q) {
-    const dlc_adamw_group& s = groups[q];
-    if (!(std::isfinite(s.lr) && s.lr >= 0.0 && std::isfinite(s.weight_decay) && s.weight_decay >= 0.0))
-      return fail(DLC_ERR_INVALID_ARGUMENT, "lr and weight_decay must be finite and >= 0");
-    if (!(s.beta1 >= 0.0 && s.beta1 < 1.0 && s.beta2 >= 0.0 && s.beta2 < 1.0))
-      return fail(DLC_ERR_INVALID_ARGUMENT, "betas must be in [0, 1)");
-    if (!(s.eps >= FLT_MIN && s.eps <= FLT_MAX))
-      return fail(DLC_ERR_INVALID_ARGUMENT, "eps must be a normal positive fp32 number");
-    a.group[q] = {s.lr, s.beta1, s.beta2, s.eps, s.weight_decay};
-  }
-  if (group_of) {
-    for (int32_t t = 0; t < n_tensors; ++t)
-      if (group_of[t] < 0 || group_of[t] >= n_groups)
-        return fail(DLC_ERR_INVALID_ARGUMENT, "tensor " + std::to_string(t) + ": no such group");
-  }
-  a.theta = theta_learners;
-  a.grads = grads;
-  a.m = mo.m;
-  a.v = mo.v;
-  a.m_scale = mo.m_scales;
-  a.v_scale = mo.v_scales;
-  a.working = working;
-  a.steps = steps;
-  a.grad_scale = grad_scale;
-  a.lr_scale = lr_scale;
-  a.stride = learner_stride;
-  a.seed = mo.seed;
-  const hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  const InnerPartition p = adamw_partition(tensors, n_tensors, group_of);
-  for (const dlc::InnerGeom& g : p.launches) {
-    const hipError_t e = dlc::launch_adamw(a, grad_type, working ? working_type : dlc::kNone, mo.coded, g, s);
-    if (e != hipSuccess) return hip_fail(e, "AdamW kernel launch");
-  }
-  const hipError_t e = dlc::launch_adamw_advance(a, s);
-  if (e != hipSuccess) return hip_fail(e, "step count kernel launch");
-  return ok();
 }
 
 }  // namespace
@@ -1368,92 +1206,7 @@ int32_t dlc_rda_outer_step(float* theta_global, float* momentum, const float* th
   return rc == DLC_OK ? ok() : rc;
 }
 
-int32_t dlc_grad_norm_workspace_bytes(int32_t n_learners, const dlc_tensor* tensors, int32_t n_tensors,
-                                      size_t* bytes) {
-  return no_throw([&]() -> int32_t {
-    if (!bytes) return fail(DLC_ERR_INVALID_ARGUMENT, "bytes is NULL");
-    if (n_learners < 1 || n_learners > DLC_MAX_LEARNERS)
-      return fail(DLC_ERR_INVALID_ARGUMENT, "n_learners must be in [1, 64]");
-    const int32_t rc = check_tensors(tensors, n_tensors, 0, false);
-    if (rc != DLC_OK) return rc;
-    *bytes = round256((size_t)norm_partition(tensors, n_tensors).n_slots * n_learners * sizeof(double));
-    return ok();
-  });
-}
-
-int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stride, int32_t n_learners,
-                      const uint8_t* present, const dlc_tensor* tensors, int32_t n_tensors, double unscale,
-                      double max_norm, double* norm, double* grad_scale, void* workspace, size_t workspace_bytes,
-                      void* hip_stream) {
-  return no_throw([&]() -> int32_t {
-    dlc::NormArgs a;
-    std::memset(&a, 0, sizeof(a));
-    int32_t rc;
-    a.n_present = present_learners(n_learners, present, a.learner, &rc);
-    if (rc != DLC_OK) return rc;
-    if (!grads || !norm || !grad_scale)
-      return fail(DLC_ERR_INVALID_ARGUMENT, "grads, norm and grad_scale must not be NULL");
-    if (norm == grad_scale) return fail(DLC_ERR_INVALID_ARGUMENT, "the call's buffers must not overlap");
-    if (!aligned256(grads)) return fail(DLC_ERR_ALIGNMENT, "device pointers must be 256-byte aligned");
-    if (!aligned8(norm) || !aligned8(grad_scale))
-      return fail(DLC_ERR_ALIGNMENT, "norm and grad_scale must be 8-byte aligned");
-    rc = check_float_type(grad_type, "grad_type", true);
-    if (rc == DLC_OK) rc = check_tensors(tensors, n_tensors, learner_stride, true);
-    if (rc != DLC_OK) return rc;
-    if (!(std::isfinite(unscale) && unscale > 0.0))
-      return fail(DLC_ERR_INVALID_ARGUMENT, "unscale must be finite and > 0");
-    if (!(max_norm > 0.0)) return fail(DLC_ERR_INVALID_ARGUMENT, "max_norm must be > 0");
-    const InnerPartition p = norm_partition(tensors, n_tensors);
-    const size_t need = round256((size_t)p.n_slots * a.n_present * sizeof(double));
-    if (workspace == nullptr || workspace_bytes < need)
-      return fail(DLC_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
-    if (!aligned256(workspace)) return fail(DLC_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
-    a.grads = grads;
-    a.stride = learner_stride;
-    a.part = static_cast<double*>(workspace);
-    a.norm = norm;
-    a.grad_scale = grad_scale;
-    a.unscale = unscale;
-    a.max_norm = max_norm;
-    a.n_slots = (int32_t)p.n_slots;
-    const hipStream_t s = static_cast<hipStream_t>(hip_stream);
-    for (const dlc::InnerGeom& g : p.launches) {
-      const hipError_t e = dlc::launch_norm_partial(a, grad_type, g, s);
-      if (e != hipSuccess) return hip_fail(e, "gradient norm kernel launch");
-    }
-    const hipError_t e = dlc::launch_norm_final(a, s);
-    if (e != hipSuccess) return hip_fail(e, "gradient norm kernel launch");
-    return ok();
-  });
-}
-
-int32_t dlc_adamw_step(float* theta_learners, const void* grads, int32_t grad_type, float* exp_avg,
-                       float* exp_avg_sq, int64_t* steps, int64_t learner_stride, int32_t n_learners,
-                       const uint8_t* present, const dlc_tensor* tensors, int32_t n_tensors, const int32_t* group_of,
-                       const dlc_adamw_group* groups, int32_t n_groups, const double* grad_scale,
-                       const double* lr_scale, void* working, int32_t working_type, void* hip_stream) {
-  return no_throw([&]() -> int32_t {
-    return adamw_step(theta_learners, grads, grad_type, {exp_avg, exp_avg_sq, nullptr, nullptr, false, 0}, steps,
-                      learner_stride, n_learners, present, tensors, n_tensors, group_of, groups, n_groups, grad_scale,
-                      lr_scale, working, working_type, hip_stream);
-  });
-}
-
-int32_t dlc_adamw_coded_step(float* theta_learners, const void* grads, int32_t grad_type, uint8_t* m_codes,
-                             uint8_t* m_scales, uint8_t* v_codes, uint8_t* v_scales, int64_t* steps,
-                             int64_t learner_stride, int32_t n_learners, const uint8_t* present,
-                             const dlc_tensor* tensors, int32_t n_tensors, const int32_t* group_of,
-                             const dlc_adamw_group* groups, int32_t n_groups, uint64_t seed,
-                             const double* grad_scale, const double* lr_scale, void* working, int32_t working_type,
-                             void* hip_stream) {
-  return no_throw([&]() -> int32_t {
-    return adamw_step(theta_learners, grads, grad_type, {m_codes, v_codes, m_scales, v_scales, true, seed}, steps,
-                      learner_stride, n_learners, present, tensors, n_tensors, group_of, groups, n_groups, grad_scale,
-                      lr_scale, working, working_type, hip_stream);
-  });
-}
-
-const char* dlc_last_error(void) { return g_last_error.c_str(); }
+const char* dlc_last_error(void) { return dlc::last_error(); }
 
 const char* dlc_version(void) { return "dlc 0.1.0 (gfx950)"; }
 

@@ -1,0 +1,284 @@
+// C ABI of the learners' inner step (gradient norm, AdamW): argument checks, ranges and
+// kernel launches.  As in the rest of the library nothing here allocates device memory,
+// keeps state between calls or waits on the stream.
+#include "dlc.h"
+#include "dlc_host.h"
+#include "dlc_inner.h"
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <cstring>
+#include <string>
+#include <vector>
+
+namespace {
+
+using dlc::aligned256;
+using dlc::check_tensors;
+using dlc::fail;
+using dlc::hip_fail;
+using dlc::kMaxTensorNumel;
+using dlc::ok;
+using dlc::round256;
+
+constexpr int64_t kNormBlocks = 2048;
+constexpr int64_t kAdamWTiles = 2;
+
+struct InnerPartition {
+  std::vector<dlc::InnerGeom> launches;
+  int64_t n_slots = 0;
+};
+
+// Tensors of one group that follow each other in the row without padding become one
+// range (of at most 2^32 - 1 elements); every range gets ceil(tiles / tiles_per_block)
+// blocks, tiles_per_block at least min_tiles and such that the call has about
+// target_blocks blocks.
+InnerPartition inner_partition(const dlc_tensor* t, int32_t n, const int32_t* group_of, int64_t min_tiles,
+                               int64_t target_blocks) {
+  struct Range {
+    int64_t lo, count;
+    int32_t group;
+  };
+  std::vector<Range> ranges;
+  ranges.reserve(n);
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t group = group_of ? group_of[i] : 0;
+    if (!ranges.empty()) {
+      Range& b = ranges.back();
+      if (b.group == group && b.lo + b.count == t[i].loffset && b.count + t[i].numel <= kMaxTensorNumel) {
+        b.count += t[i].numel;
+        continue;
+      }
+    }
+    ranges.push_back({t[i].loffset, t[i].numel, group});
+  }
+  int64_t tiles = 0;
+  for (const Range& r : ranges) tiles += (r.count + dlc::kInnerTile - 1) / dlc::kInnerTile;
+  const int64_t tpb = std::max(min_tiles, (tiles + target_blocks - 1) / target_blocks);
+  InnerPartition p;
+  for (size_t s = 0; s < ranges.size(); s += dlc::kMaxRanges) {
+    dlc::InnerGeom g;
+    std::memset(&g, 0, sizeof(g));
+    g.n_ranges = (int32_t)std::min<size_t>(dlc::kMaxRanges, ranges.size() - s);
+    g.tiles_per_block = (int32_t)tpb;
+    g.slot_base = (int32_t)p.n_slots;
+    int64_t blocks = 0;
+    for (int32_t i = 0; i < g.n_ranges; ++i) {
+      const Range& r = ranges[s + i];
+      g.r[i] = {(uint32_t)(r.lo / DLC_ALIGN_ELEMS), (uint32_t)r.count, (uint32_t)blocks};
+      g.group[i] = (uint8_t)r.group;
+      blocks += (r.count + tpb * dlc::kInnerTile - 1) / (tpb * dlc::kInnerTile);
+    }
+    g.n_blocks = (int32_t)blocks;
+    p.n_slots += blocks;
+    p.launches.push_back(g);
+  }
+  return p;
+}
+
+InnerPartition norm_partition(const dlc_tensor* t, int32_t n) { return inner_partition(t, n, nullptr, 1, kNormBlocks); }
+
+// A grid's x extent times its block must stay below 2^32 threads.
+constexpr int64_t kAdamWMaxBlocks = int64_t(1) << 22;
+
+InnerPartition adamw_partition(const dlc_tensor* t, int32_t n, const int32_t* group_of) {
+  return inner_partition(t, n, group_of, kAdamWTiles, kAdamWMaxBlocks);
+}
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// The present learners' indices -> list, their number; 0 = an error was set.
+int32_t present_learners(int32_t n_learners, const uint8_t* present, uint8_t* list, int32_t* rc) {
+  *rc = DLC_OK;
+  if (n_learners < 1 || n_learners > DLC_MAX_LEARNERS) {
+    *rc = fail(DLC_ERR_INVALID_ARGUMENT, "n_learners must be in [1, 64]");
+    return 0;
+  }
+  int32_t kp = 0;
+  for (int32_t i = 0; i < n_learners; ++i) {
+    if (present == nullptr || present[i] != 0) list[kp++] = (uint8_t)i;
+  }
+  if (kp == 0) *rc = fail(DLC_ERR_NO_QUORUM, "no learner is present");
+  return kp;
+}
+
+int32_t check_float_type(int32_t type, const char* name, bool wide) {
+  if (type == DLC_BFLOAT16 || type == DLC_FLOAT16 || (wide && type == DLC_FLOAT32)) return DLC_OK;
+  return fail(DLC_ERR_INVALID_ARGUMENT, std::string(name) + " is not one of the call's types");
+}
+
+// No C++ exception crosses the ABI: running out of host memory is an error code.
+template <typename F>
+int32_t no_throw(F&& f) noexcept {
+  try {
+    return f();
+  } catch (...) {
+    return dlc::out_of_memory();
+  }
+}
+
+// The moments of an AdamW call: 32-bit, or codes and scale bytes.
+struct Moments {
+  void* m;
+  void* v;
+  uint8_t* m_scales;
+  uint8_t* v_scales;
+  bool coded;
+  uint64_t seed;
+};
+
+int32_t adamw_step(float* theta_learners, const void* grads, int32_t grad_type, const Moments& mo, int64_t* steps,
+                   int64_t learner_stride, int32_t n_learners, const uint8_t* present, const dlc_tensor* tensors,
+                   int32_t n_tensors, const int32_t* group_of, const dlc_adamw_group* groups, int32_t n_groups,
+                   const double* grad_scale, const double* lr_scale, void* working, int32_t working_type,
+                   void* hip_stream) {
+  dlc::AdamWArgs a;
+  std::memset(&a, 0, sizeof(a));
+  int32_t rc;
+  a.n_present = present_learners(n_learners, present, a.learner, &rc);
+  if (rc != DLC_OK) return rc;
+  if (!theta_learners || !grads || !mo.m || !mo.v || !steps || (mo.coded && (!mo.m_scales || !mo.v_scales)))
+    return fail(DLC_ERR_INVALID_ARGUMENT, "theta_learners, grads, the moments and steps must not be NULL");
+  const void* buffers[] = {theta_learners, grads, mo.m, mo.v, mo.m_scales, mo.v_scales, working};
+  for (const void* p : buffers) {
+    if (!aligned256(p)) return fail(DLC_ERR_ALIGNMENT, "device pointers must be 256-byte aligned");
+    if (p && std::count(std::begin(buffers), std::end(buffers), p) > 1)
+      return fail(DLC_ERR_INVALID_ARGUMENT, "the call's buffers must not overlap");
+  }
+  if (!aligned8(steps) || !aligned8(grad_scale) || !aligned8(lr_scale))
+    return fail(DLC_ERR_ALIGNMENT, "steps, grad_scale and lr_scale must be 8-byte aligned");
+  rc = check_float_type(grad_type, "grad_type", true);
+  if (rc == DLC_OK && working) rc = check_float_type(working_type, "working_type", false);
+  if (rc == DLC_OK) rc = check_tensors(tensors, n_tensors, learner_stride, true);
+  if (rc != DLC_OK) return rc;
+  if (!groups || n_groups < 1 || n_groups > DLC_MAX_GROUPS)
+    return fail(DLC_ERR_INVALID_ARGUMENT, "groups must hold 1 to 16 groups");
+  for (int32_t q = 0; q < n_groups; ++q) {
+    const dlc_adamw_group& s = groups[q];
+    if (!(std::isfinite(s.lr) && s.lr >= 0.0 && std::isfinite(s.weight_decay) && s.weight_decay >= 0.0))
+      return fail(DLC_ERR_INVALID_ARGUMENT, "lr and weight_decay must be finite and >= 0");
+    if (!(s.beta1 >= 0.0 && s.beta1 < 1.0 && s.beta2 >= 0.0 && s.beta2 < 1.0))
+      return fail(DLC_ERR_INVALID_ARGUMENT, "betas must be in [0, 1)");
+    if (!(s.eps >= FLT_MIN && s.eps <= FLT_MAX))
+      return fail(DLC_ERR_INVALID_ARGUMENT, "eps must be a normal positive fp32 number");
+    a.group[q] = {s.lr, s.beta1, s.beta2, s.eps, s.weight_decay};
+  }
+  if (group_of) {
+    for (int32_t t = 0; t < n_tensors; ++t)
+      if (group_of[t] < 0 || group_of[t] >= n_groups)
+        return fail(DLC_ERR_INVALID_ARGUMENT, "tensor " + std::to_string(t) + ": no such group");
+  }
+  a.theta = theta_learners;
+  a.grads = grads;
+  a.m = mo.m;
+  a.v = mo.v;
+  a.m_scale = mo.m_scales;
+  a.v_scale = mo.v_scales;
+  a.working = working;
+  a.steps = steps;
+  a.grad_scale = grad_scale;
+  a.lr_scale = lr_scale;
+  a.stride = learner_stride;
+  a.seed = mo.seed;
+  const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+  const InnerPartition p = adamw_partition(tensors, n_tensors, group_of);
+  for (const dlc::InnerGeom& g : p.launches) {
+    const hipError_t e = dlc::launch_adamw(a, grad_type, working ? working_type : dlc::kNone, mo.coded, g, s);
+    if (e != hipSuccess) return hip_fail(e, "AdamW kernel launch");
+  }
+  const hipError_t e = dlc::launch_adamw_advance(a, s);
+  if (e != hipSuccess) return hip_fail(e, "step count kernel launch");
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t dlc_grad_norm_workspace_bytes(int32_t n_learners, const dlc_tensor* tensors, int32_t n_tensors,
+                                      size_t* bytes) {
+  return no_throw([&]() -> int32_t {
+    if (!bytes) return fail(DLC_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    if (n_learners < 1 || n_learners > DLC_MAX_LEARNERS)
+      return fail(DLC_ERR_INVALID_ARGUMENT, "n_learners must be in [1, 64]");
+    const int32_t rc = check_tensors(tensors, n_tensors, 0, false);
+    if (rc != DLC_OK) return rc;
+    *bytes = round256((size_t)norm_partition(tensors, n_tensors).n_slots * n_learners * sizeof(double));
+    return ok();
+  });
+}
+
+int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stride, int32_t n_learners,
+                      const uint8_t* present, const dlc_tensor* tensors, int32_t n_tensors, double unscale,
+                      double max_norm, double* norm, double* grad_scale, void* workspace, size_t workspace_bytes,
+                      void* hip_stream) {
+  return no_throw([&]() -> int32_t {
+    dlc::NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    int32_t rc;
+    a.n_present = present_learners(n_learners, present, a.learner, &rc);
+    if (rc != DLC_OK) return rc;
+    if (!grads || !norm || !grad_scale)
+      return fail(DLC_ERR_INVALID_ARGUMENT, "grads, norm and grad_scale must not be NULL");
+    if (norm == grad_scale) return fail(DLC_ERR_INVALID_ARGUMENT, "the call's buffers must not overlap");
+    if (!aligned256(grads)) return fail(DLC_ERR_ALIGNMENT, "device pointers must be 256-byte aligned");
+    if (!aligned8(norm) || !aligned8(grad_scale))
+      return fail(DLC_ERR_ALIGNMENT, "norm and grad_scale must be 8-byte aligned");
+    rc = check_float_type(grad_type, "grad_type", true);
+    if (rc == DLC_OK) rc = check_tensors(tensors, n_tensors, learner_stride, true);
+    if (rc != DLC_OK) return rc;
+    if (!(std::isfinite(unscale) && unscale > 0.0))
+      return fail(DLC_ERR_INVALID_ARGUMENT, "unscale must be finite and > 0");
+    if (!(max_norm > 0.0)) return fail(DLC_ERR_INVALID_ARGUMENT, "max_norm must be > 0");
+    const InnerPartition p = norm_partition(tensors, n_tensors);
+    const size_t need = round256((size_t)p.n_slots * a.n_present * sizeof(double));
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(DLC_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
+    if (!aligned256(workspace)) return fail(DLC_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+    a.grads = grads;
+    a.stride = learner_stride;
+    a.part = static_cast<double*>(workspace);
+    a.norm = norm;
+    a.grad_scale = grad_scale;
+    a.unscale = unscale;
+    a.max_norm = max_norm;
+    a.n_slots = (int32_t)p.n_slots;
+    const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    for (const dlc::InnerGeom& g : p.launches) {
+      const hipError_t e = dlc::launch_norm_partial(a, grad_type, g, s);
+      if (e != hipSuccess) return hip_fail(e, "gradient norm kernel launch");
+    }
+    const hipError_t e = dlc::launch_norm_final(a, s);
+    if (e != hipSuccess) return hip_fail(e, "gradient norm kernel launch");
+    return ok();
+  });
+}
+
+int32_t dlc_adamw_step(float* theta_learners, const void* grads, int32_t grad_type, float* exp_avg,
+                       float* exp_avg_sq, int64_t* steps, int64_t learner_stride, int32_t n_learners,
+                       const uint8_t* present, const dlc_tensor* tensors, int32_t n_tensors, const int32_t* group_of,
+                       const dlc_adamw_group* groups, int32_t n_groups, const double* grad_scale,
+                       const double* lr_scale, void* working, int32_t working_type, void* hip_stream) {
+  return no_throw([&]() -> int32_t {
+    return adamw_step(theta_learners, grads, grad_type, {exp_avg, exp_avg_sq, nullptr, nullptr, false, 0}, steps,
+                      learner_stride, n_learners, present, tensors, n_tensors, group_of, groups, n_groups, grad_scale,
+                      lr_scale, working, working_type, hip_stream);
+  });
+}
+
+int32_t dlc_adamw_coded_step(float* theta_learners, const void* grads, int32_t grad_type, uint8_t* m_codes,
+                             uint8_t* m_scales, uint8_t* v_codes, uint8_t* v_scales, int64_t* steps,
+                             int64_t learner_stride, int32_t n_learners, const uint8_t* present,
+                             const dlc_tensor* tensors, int32_t n_tensors, const int32_t* group_of,
+                             const dlc_adamw_group* groups, int32_t n_groups, uint64_t seed,
+                             const double* grad_scale, const double* lr_scale, void* working, int32_t working_type,
+                             void* hip_stream) {
+  return no_throw([&]() -> int32_t {
+    return adamw_step(theta_learners, grads, grad_type, {m_codes, v_codes, m_scales, v_scales, true, seed}, steps,
+                      learner_stride, n_learners, present, tensors, n_tensors, group_of, groups, n_groups, grad_scale,
+                      lr_scale, working, working_type, hip_stream);
+  });
+}
+
+}  // extern "C"
