@@ -11,8 +11,8 @@
 //   m     <- beta1 m + (1 - beta1) g
 //   v     <- beta2 v + (1 - beta2) g^2
 //   theta <- (1 - eta wd) theta - eta / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
-// The moments and theta are computed in fp64 and rounded to fp32 once; the quotient
-// is an fp32 expression of the rounded moments.
+// The moments are computed in fp64 and rounded to fp32 once; the change of theta is an
+// fp32 expression of the rounded moments, subtracted from theta with one rounding.
 //
 // Coded moments: m is an e4m3 code and v an e5m2 code times a power of two shared by
 // 64 consecutive elements (an e8m0 byte), so scaling is exact and a code's relative
@@ -157,8 +157,9 @@ __device__ __forceinline__ double power(double b, uint64_t t) {
 
 // What an element's update needs besides the element: the same for a whole block.
 struct Rates {
-  double b1, c1, b2, c2, decay, clip;  // c = 1 - b
-  float size, root, eps;               // eta / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+  double b1, c1, b2, c2;  // c1 = (1 - beta1) clip, c2 = (1 - beta2) clip^2
+  float shrink;           // eta wd
+  float size, root, eps;  // eta / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
 };
 
 // A learner's gradient scale; its step is left out unless the scale is finite and positive.
@@ -172,26 +173,44 @@ __device__ __forceinline__ Rates rates_of(const InnerGroup& q, double clip, doub
   Rates r;
   const double eta = q.lr * lr_scale;
   r.b1 = q.beta1;
-  r.c1 = 1.0 - q.beta1;
+  r.c1 = (1.0 - q.beta1) * clip;
   r.b2 = q.beta2;
-  r.c2 = 1.0 - q.beta2;
-  r.decay = 1.0 - eta * q.weight_decay;
-  r.clip = clip;
+  r.c2 = (1.0 - q.beta2) * clip * clip;
+  r.shrink = (float)(eta * q.weight_decay);
   r.size = (float)(eta / (1.0 - power(q.beta1, t)));
   r.root = (float)(1.0 / sqrt(1.0 - power(q.beta2, t)));
   r.eps = (float)q.eps;
   return r;
 }
 
-__device__ __forceinline__ void update(const Rates& r, float grad, double& m, double& v, float& theta, float& m32,
-                                       float& v32) {
-  const double g = (double)grad * r.clip;
-  m = r.b1 * m + r.c1 * g;
-  v = r.b2 * v + r.c2 * g * g;
-  m32 = (float)m;
-  v32 = (float)v;
-  const float step = r.size * (m32 / (sqrtf(v32) * r.root + r.eps));  // m32 may be subnormal: it is divided first
-  theta = (float)(r.decay * (double)theta - (double)step);
+// With decimal betas the exact sums lie on fp32 rounding ties about once in a hundred
+// elements (0.8 m + 0.2 g = (4 m + g) / 5), which the last bit in fp64 then decides: each
+// product is rounded on its own, as any fp64 evaluation of the formula does.
+__device__ __forceinline__ float new_m(double b1, double c1, double m, double grad) {
+#ifdef X_FMA
+  return (float)__fma_rn(b1, m, c1 * grad);
+#else
+  return (float)(b1 * m + c1 * grad);
+#endif
+}
+
+__device__ __forceinline__ float new_v(double b2, double c2, double v, double grad) {
+#ifdef X_FMA
+  return (float)__fma_rn(b2, v, c2 * grad * grad);
+#else
+  return (float)(b2 * v + c2 * grad * grad);
+#endif
+}
+
+// theta - (eta wd theta + step).  The hardware's square root and reciprocal are within
+// one unit in the last place but take no subnormal operand: a tiny v is scaled up (eps,
+// and with it the denominator, is a normal number).  m may be subnormal, so it is
+// divided before it is scaled.
+__device__ __forceinline__ float new_theta(const Rates& r, float theta, float m, float v) {
+  const bool tiny = v < 0x1p-96f;
+  const float s = __builtin_amdgcn_sqrtf(tiny ? v * 0x1p64f : v) * (tiny ? 0x1p-32f : 1.0f);
+  const float q = m * __builtin_amdgcn_rcpf(__fmaf_rn(s, r.root, r.eps));
+  return theta - __fmaf_rn(r.shrink, theta, r.size * q);
 }
 
 template <typename G, typename W>
@@ -216,8 +235,9 @@ __global__ __launch_bounds__(kInnerBlock) void k_adamw(const AdamWArgs a, const 
     load4(v + e, n, vv);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      double md = mm[c], vd = vv[c];
-      update(r, gr[c], md, vd, th[c], mm[c], vv[c]);
+      mm[c] = new_m(r.b1, r.c1, mm[c], gr[c]);
+      vv[c] = new_v(r.b2, r.c2, vv[c], gr[c]);
+      th[c] = new_theta(r, th[c], mm[c], vv[c]);
     }
     store4(theta + e, n, th);
     store4(m + e, n, mm);
@@ -241,9 +261,9 @@ struct Keys {
 };
 
 // i + 64 * (e >> 32) names the learner and the 2^32 elements that e is among.
-__device__ __forceinline__ Keys keys_of(uint64_t seed, uint64_t t, int learner, int64_t e) {
+__device__ __forceinline__ Keys keys_of(uint64_t seed, uint64_t t, int learner, uint32_t e_high) {
   Keys k;
-  k.k1 = mix(mix((uint32_t)seed + (uint32_t)t) + (uint32_t)learner + 64u * (uint32_t)(e >> 32));
+  k.k1 = mix(mix((uint32_t)seed + (uint32_t)t) + (uint32_t)learner + 64u * e_high);
   k.k2 = mix(k.k1 + (uint32_t)(seed >> 32) + (uint32_t)t);
   return k;
 }
@@ -255,36 +275,34 @@ __device__ __forceinline__ uint32_t random_bits(const Keys& k, uint32_t e) {
   return x ^ (x >> 16);
 }
 
-// A format with kMantissa bits and exponent bias kBias; a block's scale byte puts the
-// exponent of its largest value at kTop, so that no value reaches the format's end,
-// rounded up or not.
-template <int kMantissa, int kBias, int kTop>
-struct Code {
-  static constexpr int kCut = 23 - kMantissa;
+// A block's scale byte puts the exponent of its largest value at 2^7 (e4m3, which ends at
+// 448) or 2^14 (e5m2, 57344), so that no value reaches the format's end, rounded up or not.
+constexpr int kTopM = 7, kTopV = 14;
+constexpr uint32_t kNaNs = 0x7F7F7F7Fu;  // four NaNs of either format
+constexpr float kLeastV = 0x1p-16f;  // the smallest e5m2 number
 
-  // The block's scale byte, from the largest finite magnitude among its elements.
-  static __device__ __forceinline__ int scale_byte(float largest) {
-    const int b = (int)(__float_as_uint(largest) >> 23) - kTop;
-    return b > 0 ? b : 0;
-  }
+__device__ __forceinline__ uint32_t scale_byte(uint32_t largest, int top) {
+  const int b = (int)(largest >> 23) - top;
+  return b > 0 ? b : 0;
+}
 
-  // |x| / scale, cut to the code's grid after adding r16 + 1/2 units of 2^-16 of the
-  // grid's step.  Below the smallest normal number the grid is that of the number
-  // itself: adding it aligns the bits.
-  static __device__ __forceinline__ uint32_t encode(float x, int byte, uint32_t r16) {
-    const float y = fabsf(x) * __uint_as_float((uint32_t)(254 - byte) << 23);
-    constexpr float kLeast = 1.0f / (float)(1 << (kBias - 1));
-    const bool small = y < kLeast;
-    const uint32_t b = __float_as_uint(small ? y + kLeast : y) + (r16 << (kCut - 16)) + (1u << (kCut - 17));
-    const uint32_t code = (b >> kCut) - (uint32_t)((small ? 128 - kBias : 127 - kBias) << kMantissa);
-    return __builtin_isfinite(x) ? code : 0x7Fu;
-  }
-};
-using CodeM = Code<3, 7, 7>;    // e4m3
-using CodeV = Code<2, 15, 14>;  // e5m2
+// 2^(127 - byte): at most 2^127, at least 2^-120
+__device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-  return byte != 0 ? __uint_as_float(byte << 23) : __uint_as_float(1u << 22);  // 2^(byte - 127)
+// beta * 2^(byte - 127), exact
+__device__ __forceinline__ double scaled(double beta, uint32_t byte) { return ldexp(beta, (int)byte - 127); }
+
+// The hardware's stochastic conversions add a random word below the code's last bit (from
+// its top 20 bits for e4m3, 21 for e5m2) and cut; the word here is 16 random bits and a
+// half.  kByte: the byte of `word` that takes the code.
+template <int kByte>
+__device__ __forceinline__ void code_m(uint32_t& word, float y, uint32_t bits) {
+  word = __builtin_amdgcn_cvt_sr_fp8_f32(y, (int)(bits << 16 | 0x8000u), (int)word, kByte);
+}
+
+template <int kByte>
+__device__ __forceinline__ void code_v(uint32_t& word, float y, uint32_t bits) {
+  word = __builtin_amdgcn_cvt_sr_bf8_f32(y, (int)((bits & 0xFFFF0000u) | 0x8000u), (int)word, kByte);
 }
 
 // Four codes of a word as floats.
@@ -319,11 +337,29 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t n, uint32_t w) {
   }
 }
 
-// The largest over the 16 lanes that hold a block of 64 elements.
-__device__ __forceinline__ float block_largest(float x) {
-#pragma unroll
-  for (int m = 8; m >= 1; m >>= 1) x = fmaxf(x, __shfl_xor(x, m, 64));
+// The largest over the 16 lanes (one row of the data-parallel primitives) that hold a
+// block of 64 elements.
+__device__ __forceinline__ uint32_t block_largest(uint32_t x) {
+  const auto step = [&](auto ctrl) {
+    const uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, decltype(ctrl)::value, 0xF, 0xF, true);
+    x = x > y ? x : y;
+  };
+  step(std::integral_constant<int, 0xB1>());   // lanes 1 0 3 2 of each four
+  step(std::integral_constant<int, 0x4E>());   // 2 3 0 1
+  step(std::integral_constant<int, 0x141>());  // each eight mirrored
+  step(std::integral_constant<int, 0x140>());  // each sixteen mirrored
   return x;
+}
+
+constexpr uint32_t kInfinity = 0x7F800000u;
+
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// A magnitude for the block's maximum: 0 where it is not finite.
+__device__ __forceinline__ uint32_t finite_magnitude(float x) { return magnitude(x) < kInfinity ? magnitude(x) : 0u; }
+
+__device__ __forceinline__ uint32_t max4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return max(max(a, b), max(c, d));
 }
 
 template <typename G, typename W>
@@ -342,6 +378,7 @@ __global__ __launch_bounds__(kInnerBlock) void k_adamw_coded(const AdamWArgs a, 
   uint8_t* ms = a.m_scale + row / kCodeBlock;
   uint8_t* vs = a.v_scale + row / kCodeBlock;
   const G* grad = (const G*)a.grads + row;
+  const Keys first = keys_of(a.seed, t, i, (uint32_t)(sp.begin >> 32));
   // every lane takes part in its block's maximum, so the trip count is the block's
   for (int64_t base = sp.begin; base < sp.end; base += 4 * kInnerBlock) {
     const int64_t e = base + 4 * threadIdx.x;
@@ -352,32 +389,49 @@ __global__ __launch_bounds__(kInnerBlock) void k_adamw_coded(const AdamWArgs a, 
     load4(grad + e, n, gr);
     decode_m(load_codes(m + e, n), mm);
     decode_v(load_codes(v + e, n), vv);
-    const double mscale = scale_value(any ? ms[e / kCodeBlock] : 0);
-    const double vscale = scale_value(any ? vs[e / kCodeBlock] : 0);
-    const Keys k = keys_of(a.seed, t, i, e);
-    float mmax = 0.0f, vmax = 0.0f;
+    const double b1 = scaled(r.b1, any ? ms[e / kCodeBlock] : 0);
+    const double b2 = scaled(r.b2, any ? vs[e / kCodeBlock] : 0);
+    Keys k = first;
+    if ((uint32_t)e < (uint32_t)sp.begin) k = keys_of(a.seed, t, i, (uint32_t)(e >> 32));  // past a multiple of 2^32
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      double md = mm[c] * mscale, vd = vv[c] * vscale;
-      update(r, gr[c], md, vd, th[c], mm[c], vv[c]);
-      if (c < n && __builtin_isfinite(mm[c])) mmax = fmaxf(mmax, fabsf(mm[c]));
-      if (c < n && __builtin_isfinite(vv[c])) vmax = fmaxf(vmax, vv[c]);
+      mm[c] = new_m(b1, r.c1, mm[c], gr[c]);
+      vv[c] = new_v(b2, r.c2, vv[c], gr[c]);
+      th[c] = new_theta(r, th[c], mm[c], vv[c]);
+      if (c >= n) mm[c] = vv[c] = 0.0f;  // not the tensor's: no part of the block's maximum
     }
-    const int mb = CodeM::scale_byte(block_largest(mmax));
-    const int vb = CodeV::scale_byte(block_largest(vmax));
+    uint32_t mtop = block_largest(max4(magnitude(mm[0]), magnitude(mm[1]), magnitude(mm[2]), magnitude(mm[3])));
+    uint32_t vtop = block_largest(max4(magnitude(vv[0]), magnitude(vv[1]), magnitude(vv[2]), magnitude(vv[3])));
+    uint32_t mbad = 0, vbad = 0;
+    if (__any(max(mtop, vtop) >= kInfinity)) {  // some value is not finite: it becomes NaN, the maximum is the others'
+      mtop = block_largest(max4(finite_magnitude(mm[0]), finite_magnitude(mm[1]), finite_magnitude(mm[2]),
+                                finite_magnitude(mm[3])));
+      vtop = block_largest(max4(finite_magnitude(vv[0]), finite_magnitude(vv[1]), finite_magnitude(vv[2]),
+                                finite_magnitude(vv[3])));
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (magnitude(mm[c]) >= kInfinity) mbad |= 0xFFu << (8 * c);
+        if (magnitude(vv[c]) >= kInfinity) vbad |= 0xFFu << (8 * c);
+      }
+    }
+    const uint32_t mb = scale_byte(mtop, kTopM), vb = scale_byte(vtop, kTopV);
+    const float mi = inverse_scale(mb), vi = inverse_scale(vb);
+    float vy[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float y = vv[c] * vi;
+      vy[c] = vv[c] > 0.0f && y < kLeastV ? kLeastV : y;  // a positive v is not coded as 0
+    }
     uint32_t mw = 0, vw = 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t bits = random_bits(k, (uint32_t)e + c);
-      const uint32_t mc = CodeM::encode(mm[c], mb, bits & 0xFFFFu) | ((__float_as_uint(mm[c]) >> 24) & 0x80u);
-      uint32_t vc = CodeV::encode(vv[c], vb, bits >> 16);
-      if (vc == 0 && vv[c] > 0.0f) vc = 1;
-      mw |= mc << (8 * c);
-      vw |= vc << (8 * c);
-    }
+    const uint32_t w0 = random_bits(k, (uint32_t)e), w1 = random_bits(k, (uint32_t)e + 1);
+    const uint32_t w2 = random_bits(k, (uint32_t)e + 2), w3 = random_bits(k, (uint32_t)e + 3);
+    code_m<0>(mw, mm[0] * mi, w0), code_v<0>(vw, vy[0], w0);
+    code_m<1>(mw, mm[1] * mi, w1), code_v<1>(vw, vy[1], w1);
+    code_m<2>(mw, mm[2] * mi, w2), code_v<2>(vw, vy[2], w2);
+    code_m<3>(mw, mm[3] * mi, w3), code_v<3>(vw, vy[3], w3);
     store4(theta + e, n, th);
-    store_codes(m + e, n, mw);
-    store_codes(v + e, n, vw);
+    store_codes(m + e, n, (mw & ~mbad) | (kNaNs & mbad));
+    store_codes(v + e, n, (vw & ~vbad) | (kNaNs & vbad));
     if (any && e % kCodeBlock == 0) {
       ms[e / kCodeBlock] = (uint8_t)mb;
       vs[e / kCodeBlock] = (uint8_t)vb;

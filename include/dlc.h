@@ -511,8 +511,9 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
  *            - eta / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *   working <- theta rounded to working_type (nearest even)
  *   steps[i] <- t
- * m, v and theta are computed in fp64 and rounded to fp32 once; the quotient is an
- * fp32 expression of the rounded moments, within 2^-20 of its value.
+ * m and v are computed in fp64 and rounded to fp32 once; the change of theta is an
+ * fp32 expression of the rounded moments, within 2^-20 of its value, and is
+ * subtracted with one rounding.
  *   theta_learners  device fp32 [n_learners][learner_stride], updated in place
  *   grads       as dlc_grad_norm
  *   exp_avg     device fp32 [n_learners][learner_stride]: m (start with zeros)
@@ -553,7 +554,7 @@ int32_t dlc_adamw_step(float* theta_learners, const void* grads, int32_t grad_ty
  *   s    = max(E - 7, 0) for m, max(E - 14, 0) for v
  *   y    = |x| * 2^(127 - s)
  *   code = sign and floor(y / u + (r + 1/2) / 2^16) * u, u the format's step at y
- *          (below the smallest normal number, y is first rounded to a multiple of
+ *          (below the smallest normal number, y is first cut to a multiple of
  *          2^-20 u for m and 2^-21 u for v)
  * with r the low (m) or high (v) 16 bits of the element's random word
  *   x0 = e + k1;  x1 = (x0 ^ x0 >> 16) * 0x9E3779B9 + k2;

@@ -141,7 +141,7 @@ def encode_blocks(fmt, x, r16):
     u = np.ldexp(1.0, e - fmt.mantissa)
     below = y < 2.0 ** fmt.least
     fine = u * 2.0 ** -(23 - fmt.mantissa)
-    y = np.where(below, np.rint(y / fine) * fine, y)
+    y = np.where(below, np.floor(y / fine) * fine, y)
     q = np.floor(y / u + (r16.astype(np.float64) + 0.5) / 65536).astype(np.int64)  # in units of u
     # a value's code: its exponent's first code plus how many steps it is above; the next binade follows on
     code = np.where(below, q, ((e - fmt.least + 1) << fmt.mantissa) + q - (1 << fmt.mantissa))

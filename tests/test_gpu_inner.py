@@ -4,8 +4,10 @@ Every buffer is filled with a sentinel outside the elements the call may touch, 
 sentinels are compared afterwards: padding between tensors, absent learners, the ends
 of rows.  Tolerances, from the definitions in include/dlc.h:
 
-  * moments: the same fp64 products and sums, rounded once: bit-identical (so are codes);
-  * theta: two roundings to fp32 of values that differ by the quotient's 2^-20:
+  * moments: the same fp64 sums, a few 2^-53 apart, rounded to fp32 once: equal but where
+    one straddles a rounding boundary, once in some 2^28 elements: equal on these inputs
+    (and so are the codes);
+  * theta: two roundings to fp32 of values that differ by the change's 2^-20:
     |theta| 2^-23 + |step| 2^-20, and the smallest subnormal;
   * the working copy: torch's rounding of the call's own theta, bit for bit;
   * norms: fp64 sums of at most 2^26 terms in some order: relative 2^-25 and less is seen as
