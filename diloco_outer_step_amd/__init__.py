@@ -152,8 +152,11 @@ class TensorList(tuple):
 
     def __new__(cls, tensors: Sequence[Tuple[int, int, int]]):
         self = super().__new__(cls, tensors)
-        self._c = _tensors(tuple(self))
-        self._ends = _extents(tuple(self))
+        plain = tuple(self)
+        self._c, self._ends = _tensors(plain), (0, 0)
+        if plain:
+            a = np.frombuffer(self._c[0], dtype=np.int64).reshape(-1, 3)
+            self._ends = tuple(int(x) for x in (a[:, :2] + a[:, 2:]).max(0))
         return self
 
 
@@ -629,39 +632,70 @@ def outputs_for(n_learners: int, learner_stride: int, n_tensors: int, device="cu
 _FLOAT_TYPES = {torch.float32: DLC_FLOAT32, torch.bfloat16: DLC_BFLOAT16, torch.float16: DLC_FLOAT16}
 
 
+_WORKING_TYPES = {torch.bfloat16: DLC_BFLOAT16, torch.float16: DLC_FLOAT16}
+
+
 def _float_type(t, name: str, types) -> int:
     """The C ABI's number of t's element type."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
     if t.dtype not in types:
         raise ValueError(f"{name} must be one of {', '.join(map(str, types))}, not {t.dtype}")
-    return _FLOAT_TYPES[t.dtype]
+    return types[t.dtype]
 
 
-def _per_learner(c: _Checks, t, name: str, k: int, dtype: torch.dtype):
-    c.need(t, name, dtype)
-    if tuple(t.shape) != (k,):
-        raise ValueError(f"{name} must have shape ({k},), not {tuple(t.shape)}")
+def _check_buffers(bufs):
+    """Each (name, tensor, dtype, shape) as the call needs it, all on one GPU.  A step of a
+    small model takes less time than naming what is wrong with it: one pass of plain
+    tests first, the naming checks only where it fails."""
+    dev = bufs[0][1].get_device()
+    for _, t, dtype, shape in bufs:
+        if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_contiguous()
+                or t.get_device() != dev or dev < 0):
+            break
+    else:
+        return
+    c = _Checks()
+    for name, t, dtype, shape in bufs:
+        c.need(t, name, dtype)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    c.done()
+
+
+def _row_shape(t, tensors, name: str) -> Tuple[int, int]:
+    """(K, learner_stride) of a [K, learner_stride] tensor whose rows hold every tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a [K, learner_stride] tensor")
+    if _extents(tensors)[1] > t.shape[1]:
+        raise ValueError(f"a tensor reaches past {name}'s row length {t.shape[1]}")
+    return t.shape
 
 
 class _OnDevice:
-    """The buffers' device made current for the call where it is not, and the stream
-    on it: the caller's, or that device's current one."""
+    """The buffers' device made current for the call where it is not, and the handle of the
+    stream on it: the caller's, or that device's current one."""
 
-    def __init__(self, device: torch.device, stream):
-        if isinstance(stream, torch.cuda.Stream) and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the call's buffers on {device}")
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.stream = stream
+    def __init__(self, index: int, stream):
+        if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the call's buffers on cuda:{index}")
+        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+        self.index, self.stream = index, stream
 
-    def __enter__(self):
+    def __enter__(self) -> int:
         if self.guard is not None:
             self.guard.__enter__()
-        return _stream(self.stream)
+        if self.stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.index)
+        return _stream(self.stream).value or 0
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
+
+
+def _address(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def group_ids(group_of: Sequence[int]) -> np.ndarray:
@@ -686,24 +720,19 @@ def dlc_grad_norm(grads, tensors, norm, grad_scale, workspace, max_norm=float("i
     """Every present learner's gradient norm, times `unscale`, into norm, and the factor
     that unscales and clips its gradients into grad_scale (0 where the norm is not
     finite); both device fp64 [K].  grads: [K, learner_stride] fp32, bf16 or fp16."""
-    gt = _float_type(grads, "grads", tuple(_FLOAT_TYPES))
-    if grads.dim() != 2:
-        raise ValueError("grads must be a [K, learner_stride] tensor")
-    k, stride = grads.shape
+    k, stride = _row_shape(grads, tensors, "grads")
+    gt = _float_type(grads, "grads", _FLOAT_TYPES)
     _present_list(present, k)
-    c = _Checks()
-    c.need(grads, "grads", grads.dtype)
-    if _extents(tensors)[1] > stride:
-        raise ValueError(f"a tensor reaches past learner_stride {stride}")
-    _per_learner(c, norm, "norm", k, torch.float64)
-    _per_learner(c, grad_scale, "grad_scale", k, torch.float64)
-    c.workspace(workspace)
-    c.done()
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError(f"workspace must be a torch.Tensor, not {type(workspace).__name__}")
+    _check_buffers((("grads", grads, grads.dtype, (k, stride)), ("norm", norm, torch.float64, (k,)),
+                    ("grad_scale", grad_scale, torch.float64, (k,)),
+                    ("workspace", workspace, torch.uint8, workspace.shape)))
     arr, n = _tensors(tensors)
     _buf, pres = _present(present, k)
-    with _OnDevice(grads.device, stream) as s:
-        _check(_lib.dlc_grad_norm(_ptr(grads), gt, stride, k, pres, arr, n, float(unscale), float(max_norm),
-                                  _ptr(norm), _ptr(grad_scale), _ptr(workspace), workspace.numel(), s))
+    with _OnDevice(grads.get_device(), stream) as s:
+        _check(_lib.dlc_grad_norm(grads.data_ptr(), gt, stride, k, pres, arr, n, float(unscale), float(max_norm),
+                                  norm.data_ptr(), grad_scale.data_ptr(), workspace.data_ptr(), workspace.numel(), s))
 
 
 def coded_moments(n_learners: int, learner_stride: int, device="cuda"):
@@ -719,37 +748,36 @@ def coded_moments(n_learners: int, learner_stride: int, device="cuda"):
 
 def _adamw(theta_L, grads, moments, steps, tensors, groups, group_of, grad_scale, lr_scale, working, present):
     """Buffer checks of an AdamW call -> the arguments its two forms share.  moments:
-    (name, tensor, dtype, row length as a fraction of the learner's) each."""
-    c = _Checks()
-    k, stride = c.learners(theta_L, tensors)
+    (name, tensor, dtype, elements per value) each."""
+    k, stride = _row_shape(theta_L, tensors, "theta_L")
     _present_list(present, k)
-    gt = _float_type(grads, "grads", tuple(_FLOAT_TYPES))
-    c.rows(grads, "grads", k, stride, grads.dtype)
+    gt, wt = _float_type(grads, "grads", _FLOAT_TYPES), DLC_FLOAT32
+    rows, per_learner = (k, stride), (k,)
+    bufs = [("theta_L", theta_L, torch.float32, rows), ("grads", grads, grads.dtype, rows),
+            ("steps", steps, torch.int64, per_learner)]
     for name, t, dtype, per in moments:
-        c.rows(t, name, k, stride // per, dtype)
-    _per_learner(c, steps, "steps", k, torch.int64)
+        bufs.append((name, t, dtype, (k, stride // per)))
     if grad_scale is not None:
-        _per_learner(c, grad_scale, "grad_scale", k, torch.float64)
+        bufs.append(("grad_scale", grad_scale, torch.float64, per_learner))
     if lr_scale is not None:
-        _per_learner(c, lr_scale, "lr_scale", k, torch.float64)
-    wt = DLC_FLOAT32
+        bufs.append(("lr_scale", lr_scale, torch.float64, per_learner))
     if working is not None:
-        wt = _float_type(working, "working", (torch.bfloat16, torch.float16))
-        c.rows(working, "working", k, stride, working.dtype)
+        wt = _float_type(working, "working", _WORKING_TYPES)
+        bufs.append(("working", working, working.dtype, rows))
     if isinstance(groups, AdamWGroup):
         groups = (groups,)
-    gs = (_Group * max(1, len(groups)))(*[tuple(g) for g in groups])
+    gs = (_Group * max(1, len(groups)))(*groups)
     ids = None
     if group_of is not None:
         ids = group_ids(group_of)
         if ids.shape != (len(tensors),):
             raise ValueError(f"group_of holds {ids.size} values for {len(tensors)} tensors")
-    c.done()
+    _check_buffers(bufs)
     arr, n = _tensors(tensors)
     buf, pres = _present(present, k)
     keep = (buf, ids)  # alive until the call returns
-    return (gt, stride, k, pres, arr, n, None if ids is None else ctypes.c_void_p(ids.ctypes.data), gs, len(groups),
-            _ptr(grad_scale), _ptr(lr_scale), _ptr(working), wt, keep)
+    return (gt, stride, k, pres, arr, n, None if ids is None else ids.ctypes.data, gs, len(groups),
+            _address(grad_scale), _address(lr_scale), _address(working), wt, keep)
 
 
 def dlc_adamw_step(theta_L, grads, exp_avg, exp_avg_sq, steps, tensors, groups=AdamWGroup(), group_of=None,
@@ -763,9 +791,9 @@ def dlc_adamw_step(theta_L, grads, exp_avg, exp_avg_sq, steps, tensors, groups=A
     gt, stride, k, pres, arr, n, ids, gs, ng, scale, lrs, work, wt, _keep = _adamw(
         theta_L, grads, (("exp_avg", exp_avg, torch.float32, 1), ("exp_avg_sq", exp_avg_sq, torch.float32, 1)), steps,
         tensors, groups, group_of, grad_scale, lr_scale, working, present)
-    with _OnDevice(theta_L.device, stream) as s:
-        _check(_lib.dlc_adamw_step(_ptr(theta_L), _ptr(grads), gt, _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(steps),
-                                   stride, k, pres, arr, n, ids, gs, ng, scale, lrs, work, wt, s))
+    with _OnDevice(theta_L.get_device(), stream) as s:
+        _check(_lib.dlc_adamw_step(theta_L.data_ptr(), grads.data_ptr(), gt, exp_avg.data_ptr(), exp_avg_sq.data_ptr(),
+                                   steps.data_ptr(), stride, k, pres, arr, n, ids, gs, ng, scale, lrs, work, wt, s))
 
 
 def dlc_adamw_coded_step(theta_L, grads, m_codes, m_scales, v_codes, v_scales, steps, tensors, groups=AdamWGroup(),
@@ -781,7 +809,8 @@ def dlc_adamw_coded_step(theta_L, grads, m_codes, m_scales, v_codes, v_scales, s
         (("m_codes", m_codes, torch.float8_e4m3fn, 1), ("m_scales", m_scales, torch.uint8, DLC_CODE_BLOCK),
          ("v_codes", v_codes, torch.float8_e5m2, 1), ("v_scales", v_scales, torch.uint8, DLC_CODE_BLOCK)),
         steps, tensors, groups, group_of, grad_scale, lr_scale, working, present)
-    with _OnDevice(theta_L.device, stream) as s:
-        _check(_lib.dlc_adamw_coded_step(_ptr(theta_L), _ptr(grads), gt, _ptr(m_codes), _ptr(m_scales),
-                                         _ptr(v_codes), _ptr(v_scales), _ptr(steps), stride, k, pres, arr, n, ids, gs,
-                                         ng, int(seed), scale, lrs, work, wt, s))
+    with _OnDevice(theta_L.get_device(), stream) as s:
+        _check(_lib.dlc_adamw_coded_step(theta_L.data_ptr(), grads.data_ptr(), gt, m_codes.data_ptr(),
+                                         m_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                                         steps.data_ptr(), stride, k, pres, arr, n, ids, gs, ng, int(seed), scale, lrs,
+                                         work, wt, s))

@@ -14,11 +14,18 @@
 
 namespace dlc {
 
-constexpr int kMaxRanges = 236;
+constexpr int kMaxRanges = 216;
 constexpr int kMaxGroups = 16;
-constexpr int kInnerBlock = 256;                      // threads per block
-constexpr int kInnerTile = 4096;                      // elements per tile
-constexpr int kCodeBlock = 64;                        // elements that share a scale byte
+constexpr int kCodeBlock = 64;       // elements that share a scale byte
+// AdamW: a block takes one tile, its threads kAdamWQuads (kCodedQuads) times four elements each.
+constexpr int kAdamWBlock = 128;
+constexpr int kAdamWQuads = 1;
+constexpr int kCodedQuads = 2;
+// Gradient norm: a block takes whole steps of kNormBlock threads times kNormLoads 16-byte loads.
+constexpr int kNormBlock = 256;
+constexpr int kNormLoads = 4;
+constexpr int kNormStep = kNormBlock * kNormLoads * 4;  // elements, fp32
+constexpr int kNormFinal = 1024;     // threads of the final sum
 
 enum FloatType : int32_t { kF32 = 0, kBF16 = 1, kF16 = 2, kNone = -1 };
 
@@ -31,7 +38,7 @@ struct InnerRange {
 struct InnerGeom {
   int32_t n_ranges;
   int32_t n_blocks;
-  int32_t tiles_per_block;
+  int64_t per_block;     // elements per block
   int32_t slot_base;     // the launch's first slot of block partials
   InnerRange r[kMaxRanges];
   uint8_t group[kMaxRanges];
@@ -39,6 +46,7 @@ struct InnerGeom {
 
 struct InnerGroup {
   double lr, beta1, beta2, eps, weight_decay;
+  double log_beta1, log_beta2;  // natural logarithms
 };
 
 struct AdamWArgs {
@@ -55,6 +63,7 @@ struct AdamWArgs {
   int64_t stride;
   uint64_t seed;
   int32_t n_present;
+  int32_t tickets;            // blocks per learner where the kernel counts the step itself, else 0
   uint8_t learner[64];        // present position -> learner
   InnerGroup group[kMaxGroups];
 };
@@ -62,7 +71,7 @@ struct AdamWArgs {
 struct NormArgs {
   const void* grads;
   int64_t stride;
-  double* part;               // [slot][n_present] sums of squares
+  double* part;               // [present][slot] sums of squares
   double* norm;               // [n_learners]
   double* grad_scale;         // [n_learners]
   double unscale, max_norm;
@@ -76,6 +85,8 @@ static_assert(sizeof(AdamWArgs) + sizeof(InnerGeom) <= 4096 && sizeof(NormArgs) 
 
 // Kernel launchers (dlc_inner.hip).  Each returns hipSuccess or the launch error.
 hipError_t launch_norm_partial(const NormArgs& a, int32_t grad_type, const InnerGeom& g, hipStream_t s);
+// one kernel: a block per learner over all of its ranges, and the final step
+hipError_t launch_norm_small(const NormArgs& a, int32_t grad_type, const InnerGeom& g, hipStream_t s);
 hipError_t launch_norm_final(const NormArgs& a, hipStream_t s);
 hipError_t launch_adamw(const AdamWArgs& a, int32_t grad_type, int32_t working_type, bool coded, const InnerGeom& g,
                         hipStream_t s);

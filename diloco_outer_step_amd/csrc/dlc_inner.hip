@@ -31,13 +31,15 @@ namespace {
 typedef float vf4 __attribute__((ext_vector_type(4)));
 typedef unsigned int vu2 __attribute__((ext_vector_type(2)));
 
-// Block -> (range, first and one past last element of the row).
-struct RowSpan {
+// Block -> (range, first element of the row, elements).  The launch geometry lives in the
+// kernel arguments; the search index is uniform across the block (scalar loads).
+struct Spot {
   int range;
-  int64_t begin, end;
+  int64_t base;
+  int64_t count;
 };
 
-__device__ __forceinline__ RowSpan row_span(const InnerGeom& g) {
+__device__ __forceinline__ Spot spot(const InnerGeom& g) {
   const uint32_t b = blockIdx.x;
   int lo = 0, hi = g.n_ranges - 1;
   while (lo < hi) {
@@ -45,18 +47,16 @@ __device__ __forceinline__ RowSpan row_span(const InnerGeom& g) {
     if (g.r[mid].block_first <= b) lo = mid; else hi = mid - 1;
   }
   const InnerRange r = g.r[lo];
-  RowSpan s;
+  const int64_t first = (int64_t)(b - r.block_first) * g.per_block;
+  Spot s;
   s.range = lo;
-  const int64_t per_block = (int64_t)g.tiles_per_block * kInnerTile;
-  const int64_t first = (int64_t)(b - r.block_first) * per_block;
-  const int64_t last = first + per_block < (int64_t)r.count ? first + per_block : (int64_t)r.count;
-  s.begin = (int64_t)r.lo64 * 64 + first;
-  s.end = (int64_t)r.lo64 * 64 + last;
+  s.base = (int64_t)r.lo64 * 64 + first;
+  s.count = (int64_t)r.count - first < g.per_block ? (int64_t)r.count - first : g.per_block;
   return s;
 }
 
 // Four elements at p, the first n of them valid (n may be <= 0 or >= 4); others read as 0.
-__device__ __forceinline__ void load4(const float* p, int64_t n, float (&x)[4]) {
+__device__ __forceinline__ void load4(const float* p, int n, float (&x)[4]) {
   if (n >= 4) {
     const vf4 q = __builtin_nontemporal_load((const vf4*)p);
 #pragma unroll
@@ -68,7 +68,7 @@ __device__ __forceinline__ void load4(const float* p, int64_t n, float (&x)[4]) 
 }
 
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, int64_t n, float (&x)[4]) {
+__device__ __forceinline__ void load4(const T* p, int n, float (&x)[4]) {
   typedef T v4 __attribute__((ext_vector_type(4)));
   if (n >= 4) {
     const v4 q = __builtin_nontemporal_load((const v4*)p);
@@ -81,7 +81,7 @@ __device__ __forceinline__ void load4(const T* p, int64_t n, float (&x)[4]) {
 }
 
 template <typename T>
-__device__ __forceinline__ void store4(T* p, int64_t n, const float (&x)[4]) {
+__device__ __forceinline__ void store4(T* p, int n, const float (&x)[4]) {
   typedef T v4 __attribute__((ext_vector_type(4)));
   if (n >= 4) {
     v4 q;
@@ -96,46 +96,89 @@ __device__ __forceinline__ void store4(T* p, int64_t n, const float (&x)[4]) {
   }
 }
 
+// Four gradients as they lie in memory, the first n of them valid.
+template <typename G>
+struct Raw4 {
+  typedef G v4 __attribute__((ext_vector_type(4)));
+  v4 q;
+  __device__ __forceinline__ void load(const G* p, int n) {
+    if (n >= 4) {
+      q = __builtin_nontemporal_load((const v4*)p);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) q[c] = c < n ? p[c] : (G)0.0f;
+    }
+  }
+  __device__ __forceinline__ float value(int c) const { return (float)q[c]; }
+};
+
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
   return v;
 }
 
-// The block's sum of v, in thread 0.
+// The block's sum of v, in every thread.
+template <int kThreads>
 __device__ __forceinline__ double block_sum(double v) {
-  __shared__ double red[kInnerBlock / 64];
+  __shared__ double red[kThreads / 64];
   v = wave_sum(v);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   double s = 0.0;
 #pragma unroll
-  for (int w = 0; w < kInnerBlock / 64; ++w) s += red[w];
+  for (int w = 0; w < kThreads / 64; ++w) s += red[w];
   return s;
 }
 
-template <typename G>
-__global__ __launch_bounds__(kInnerBlock) void k_norm_partial(const NormArgs a, const InnerGeom g) {
-  const RowSpan sp = row_span(g);
-  const G* row = (const G*)a.grads + (int64_t)a.learner[blockIdx.y] * a.stride;
-  double s = 0.0;
-  for (int64_t e = sp.begin + 4 * threadIdx.x; e < sp.end; e += 4 * kInnerBlock) {
-    float x[4];
-    load4(row + e, sp.end - e, x);
+// ---------------------------------------------------------------------------
+// The gradient norm
+// ---------------------------------------------------------------------------
+// The thread's sum of squares over `count` elements at p that the kThreads threads share,
+// 16-byte loads, U in flight.
+template <int kThreads, int U, typename G>
+__device__ __forceinline__ double squares(const G* p, int64_t count) {
+  constexpr int V = 16 / (int)sizeof(G);
+  typedef G vec __attribute__((ext_vector_type(V)));
+  constexpr int64_t kStep = (int64_t)kThreads * V * U;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  const auto add = [&](const vec& x) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) s = __fma_rn((double)x[c], (double)x[c], s);
+    for (int c = 0; c < V; ++c) {
+      const double d = (double)(float)x[c];
+      s[c & 3] = __fma_rn(d, d, s[c & 3]);
+    }
+  };
+  int64_t at = 0;
+  vec x[U];
+  const auto request = [&](int64_t from) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) x[j] = __builtin_nontemporal_load((const vec*)(p + from) + j * kThreads + threadIdx.x);
+  };
+  if (kStep <= count) request(0);
+  for (; at + kStep <= count; at += kStep) {
+    vec y[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) y[j] = x[j];
+    if (at + 2 * kStep <= count) request(at + kStep);
+#pragma unroll
+    for (int j = 0; j < U; ++j) add(y[j]);
   }
-  s = block_sum(s);
-  if (threadIdx.x == 0) a.part[(size_t)(g.slot_base + blockIdx.x) * a.n_present + blockIdx.y] = s;
+  for (int64_t e = at + (int64_t)V * threadIdx.x; e < count; e += (int64_t)V * kThreads) {
+    vec x;
+    if (count - e >= V) {
+      x = __builtin_nontemporal_load((const vec*)(p + e));
+    } else {
+#pragma unroll
+      for (int c = 0; c < V; ++c) x[c] = c < count - e ? p[e + c] : (G)0.0f;
+    }
+    add(x);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-__global__ __launch_bounds__(kInnerBlock) void k_norm_final(const NormArgs a) {
-  double s = 0.0;
-  for (int b = threadIdx.x; b < a.n_slots; b += kInnerBlock) s += a.part[(size_t)b * a.n_present + blockIdx.x];
-  s = block_sum(s);
-  if (threadIdx.x != 0) return;
-  const int i = a.learner[blockIdx.x];
-  const double n = a.unscale * sqrt(s);
+__device__ __forceinline__ void write_norm(const NormArgs& a, int i, double sum) {
+  const double n = a.unscale * sqrt(sum);
   double scale = a.unscale;
   if (n > a.max_norm) scale = a.unscale * (a.max_norm / n);
   if (!__builtin_isfinite(n)) scale = 0.0;
@@ -143,17 +186,57 @@ __global__ __launch_bounds__(kInnerBlock) void k_norm_final(const NormArgs a) {
   a.grad_scale[i] = scale;
 }
 
+template <typename G>
+__global__ __launch_bounds__(kNormBlock) void k_norm_partial(const NormArgs a, const InnerGeom g) {
+  const Spot sp = spot(g);
+  const G* row = (const G*)a.grads + (int64_t)a.learner[blockIdx.y] * a.stride;
+  const double s = block_sum<kNormBlock>(squares<kNormBlock, kNormLoads>(row + sp.base, sp.count));
+  if (threadIdx.x == 0) a.part[(size_t)blockIdx.y * a.n_slots + g.slot_base + blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(kNormFinal) void k_norm_final(const NormArgs a) {
+  const double* part = a.part + (size_t)blockIdx.x * a.n_slots;
+  double s = 0.0;
+  for (int b = threadIdx.x; b < a.n_slots; b += kNormFinal) s += part[b];
+  s = block_sum<kNormFinal>(s);
+  if (threadIdx.x == 0) write_norm(a, a.learner[blockIdx.x], s);
+}
+
+template <typename G>
+__global__ __launch_bounds__(kNormFinal) void k_norm_small(const NormArgs a, const InnerGeom g) {
+  const int i = a.learner[blockIdx.x];
+  const G* row = (const G*)a.grads + (int64_t)i * a.stride;
+  double s = 0.0;
+  for (int k = 0; k < g.n_ranges; ++k) s += squares<kNormFinal, 1>(row + (int64_t)g.r[k].lo64 * 64, g.r[k].count);
+  s = block_sum<kNormFinal>(s);
+  if (threadIdx.x == 0) write_norm(a, i, s);
+}
+
 // ---------------------------------------------------------------------------
 // AdamW
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ double power(double b, uint64_t t) {
-  double p = 1.0;
-  for (; t != 0; t >>= 1) {
-    if (t & 1) p *= b;
-    b *= b;
-  }
-  return p;
+// 1 - exp(x) for x <= 0 (x = t ln(beta), so 1 - beta^t): the series of exp(y) - 1 at
+// y = x / 64, then six doublings exp(2 y) - 1 = p (p + 2), which lose nothing to
+// cancellation.  Below x = -40 the result is 1 in every format here.
+__device__ __forceinline__ double one_minus_exp(double x) {
+  const double y = fmax(x, -40.0) * 0x1p-6;
+  double p = 1.0 / 39916800.0;  // 1 / 11!: the next term is below 2^-33 of the sum at y = -0.625
+  p = __fma_rn(p, y, 1.0 / 3628800.0);
+  p = __fma_rn(p, y, 1.0 / 362880.0);
+  p = __fma_rn(p, y, 1.0 / 40320.0);
+  p = __fma_rn(p, y, 1.0 / 5040.0);
+  p = __fma_rn(p, y, 1.0 / 720.0);
+  p = __fma_rn(p, y, 1.0 / 120.0);
+  p = __fma_rn(p, y, 1.0 / 24.0);
+  p = __fma_rn(p, y, 1.0 / 6.0);
+  p = __fma_rn(p, y, 0.5);
+  p = __fma_rn(p, y, 1.0) * y;
+#pragma unroll
+  for (int k = 0; k < 6; ++k) p = p * (p + 2.0);
+  return -p;
 }
+
+constexpr unsigned long long kTicket = 1ull << 40;  // above any step count
 
 // What an element's update needs besides the element: the same for a whole block.
 struct Rates {
@@ -177,8 +260,8 @@ __device__ __forceinline__ Rates rates_of(const InnerGroup& q, double clip, doub
   r.b2 = q.beta2;
   r.c2 = (1.0 - q.beta2) * clip * clip;
   r.shrink = (float)(eta * q.weight_decay);
-  r.size = (float)(eta / (1.0 - power(q.beta1, t)));
-  r.root = (float)(1.0 / sqrt(1.0 - power(q.beta2, t)));
+  r.size = (float)eta * __builtin_amdgcn_rcpf((float)one_minus_exp((double)t * q.log_beta1));
+  r.root = __builtin_amdgcn_rsqf((float)one_minus_exp((double)t * q.log_beta2));
   r.eps = (float)q.eps;
   return r;
 }
@@ -187,19 +270,31 @@ __device__ __forceinline__ Rates rates_of(const InnerGroup& q, double clip, doub
 // elements (0.8 m + 0.2 g = (4 m + g) / 5), which the last bit in fp64 then decides: each
 // product is rounded on its own, as any fp64 evaluation of the formula does.
 __device__ __forceinline__ float new_m(double b1, double c1, double m, double grad) {
-#ifdef X_FMA
-  return (float)__fma_rn(b1, m, c1 * grad);
-#else
   return (float)(b1 * m + c1 * grad);
-#endif
 }
 
 __device__ __forceinline__ float new_v(double b2, double c2, double v, double grad) {
-#ifdef X_FMA
-  return (float)__fma_rn(b2, v, c2 * grad * grad);
-#else
   return (float)(b2 * v + c2 * grad * grad);
-#endif
+}
+
+// The learner's step number t = steps + 1.  In calls of few blocks the blocks themselves
+// count the step: each adds a ticket above the count once all of its threads have read
+// it, and the one that draws the last ticket writes t over count and tickets.
+__device__ __forceinline__ uint64_t next_step(const AdamWArgs& a, int i) {
+  const uint64_t steps = (uint64_t)a.steps[i];
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)steps);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(steps >> 32));
+  const uint64_t t = (((uint64_t)hi << 32 | lo) & (kTicket - 1)) + 1;
+  if (a.tickets != 0) {
+    asm volatile("" : : "s"(lo), "s"(hi) : "memory");  // the count has arrived before the barrier
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      unsigned long long* s = (unsigned long long*)&a.steps[i];
+      const uint64_t drawn = __hip_atomic_fetch_add(s, kTicket, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) / kTicket;
+      if (drawn == (uint64_t)a.tickets - 1) __hip_atomic_store(s, t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  return t;
 }
 
 // theta - (eta wd theta + step).  The hardware's square root and reciprocal are within
@@ -214,36 +309,49 @@ __device__ __forceinline__ float new_theta(const Rates& r, float theta, float m,
 }
 
 template <typename G, typename W>
-__global__ __launch_bounds__(kInnerBlock) void k_adamw(const AdamWArgs a, const InnerGeom g) {
-  const RowSpan sp = row_span(g);
+__global__ __launch_bounds__(kAdamWBlock) void k_adamw(const AdamWArgs a, const InnerGeom g) {
+  constexpr int U = kAdamWQuads;
+  const Spot s = spot(g);
   const int i = a.learner[blockIdx.y];
-  const double clip = clip_of(a, i);
-  if (!takes_step(clip)) return;
-  const Rates r = rates_of(a.group[g.group[sp.range]], clip, a.lr_scale != nullptr ? a.lr_scale[i] : 1.0,
-                           (uint64_t)a.steps[i] + 1);
-  const int64_t row = (int64_t)i * a.stride;
+  const int64_t row = (int64_t)i * a.stride + s.base;
   float* theta = a.theta + row;
   float* m = (float*)a.m + row;
   float* v = (float*)a.v + row;
   const G* grad = (const G*)a.grads + row;
-  for (int64_t e = sp.begin + 4 * threadIdx.x; e < sp.end; e += 4 * kInnerBlock) {
-    const int64_t n = sp.end - e;
-    float th[4], gr[4], mm[4], vv[4];
-    load4(theta + e, n, th);
-    load4(grad + e, n, gr);
-    load4(m + e, n, mm);
-    load4(v + e, n, vv);
+  float th[U][4], mm[U][4], vv[U][4];
+  Raw4<G> gr[U];
+  const int at = (threadIdx.x >> 6) * (256 * U) + (threadIdx.x & 63) * 4;
+  const auto process = [&](auto full) {
+    const auto valid = [&](int j) { return decltype(full)::value ? 4 : (int)s.count - (at + 256 * j); };
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      mm[c] = new_m(r.b1, r.c1, mm[c], gr[c]);
-      vv[c] = new_v(r.b2, r.c2, vv[c], gr[c]);
-      th[c] = new_theta(r, th[c], mm[c], vv[c]);
+    for (int j = 0; j < U; ++j) {
+      const int e = at + 256 * j;
+      load4(theta + e, valid(j), th[j]);
+      load4(m + e, valid(j), mm[j]);
+      load4(v + e, valid(j), vv[j]);
+      gr[j].load(grad + e, valid(j));
     }
-    store4(theta + e, n, th);
-    store4(m + e, n, mm);
-    store4(v + e, n, vv);
-    if constexpr (!std::is_void_v<W>) store4((W*)a.working + row + e, n, th);
-  }
+    const double clip = clip_of(a, i);
+    if (!takes_step(clip)) return;
+    const uint64_t t = next_step(a, i);
+    const Rates r = rates_of(a.group[g.group[s.range]], clip, a.lr_scale != nullptr ? a.lr_scale[i] : 1.0, t);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int e = at + 256 * j;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mm[j][c] = new_m(r.b1, r.c1, mm[j][c], gr[j].value(c));
+        vv[j][c] = new_v(r.b2, r.c2, vv[j][c], gr[j].value(c));
+        th[j][c] = new_theta(r, th[j][c], mm[j][c], vv[j][c]);
+      }
+      store4(theta + e, valid(j), th[j]);
+      store4(m + e, valid(j), mm[j]);
+      store4(v + e, valid(j), vv[j]);
+      if constexpr (!std::is_void_v<W>) store4((W*)a.working + row + e, valid(j), th[j]);
+    }
+  };
+  if (s.count == 4 * kAdamWBlock * U) process(std::true_type());
+  else process(std::false_type());
 }
 
 // --- coded moments -----------------------------------------------------------
@@ -316,7 +424,7 @@ __device__ __forceinline__ void decode_v(uint32_t w, float (&x)[4]) {
   x[0] = a[0], x[1] = a[1], x[2] = b[0], x[3] = b[1];
 }
 
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t n) {
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int n) {
   if (n >= 4) return __builtin_nontemporal_load((const uint32_t*)p);
   uint32_t w = 0;
 #pragma unroll
@@ -326,7 +434,7 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t n) {
   return w;
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t n, uint32_t w) {
+__device__ __forceinline__ void store_codes(uint8_t* p, int n, uint32_t w) {
   if (n >= 4) {
     __builtin_nontemporal_store(w, (uint32_t*)p);
     return;
@@ -363,92 +471,110 @@ __device__ __forceinline__ uint32_t max4(uint32_t a, uint32_t b, uint32_t c, uin
 }
 
 template <typename G, typename W>
-__global__ __launch_bounds__(kInnerBlock) void k_adamw_coded(const AdamWArgs a, const InnerGeom g) {
-  const RowSpan sp = row_span(g);
+__global__ __launch_bounds__(kAdamWBlock) void k_adamw_coded(const AdamWArgs a, const InnerGeom g) {
+  const Spot s = spot(g);
   const int i = a.learner[blockIdx.y];
-  const double clip = clip_of(a, i);
-  if (!takes_step(clip)) return;
-  const uint64_t t = (uint64_t)a.steps[i] + 1;
-  const Rates r =
-      rates_of(a.group[g.group[sp.range]], clip, a.lr_scale != nullptr ? a.lr_scale[i] : 1.0, t);
-  const int64_t row = (int64_t)i * a.stride;
+  const int64_t row = (int64_t)i * a.stride + s.base;
   float* theta = a.theta + row;
   uint8_t* m = (uint8_t*)a.m + row;
   uint8_t* v = (uint8_t*)a.v + row;
   uint8_t* ms = a.m_scale + row / kCodeBlock;
   uint8_t* vs = a.v_scale + row / kCodeBlock;
   const G* grad = (const G*)a.grads + row;
-  const Keys first = keys_of(a.seed, t, i, (uint32_t)(sp.begin >> 32));
-  // every lane takes part in its block's maximum, so the trip count is the block's
-  for (int64_t base = sp.begin; base < sp.end; base += 4 * kInnerBlock) {
-    const int64_t e = base + 4 * threadIdx.x;
-    const int64_t n = sp.end - e;
-    const bool any = n > 0;
-    float th[4], gr[4], mm[4], vv[4];
-    load4(theta + e, n, th);
-    load4(grad + e, n, gr);
-    decode_m(load_codes(m + e, n), mm);
-    decode_v(load_codes(v + e, n), vv);
-    const double b1 = scaled(r.b1, any ? ms[e / kCodeBlock] : 0);
-    const double b2 = scaled(r.b2, any ? vs[e / kCodeBlock] : 0);
-    Keys k = first;
-    if ((uint32_t)e < (uint32_t)sp.begin) k = keys_of(a.seed, t, i, (uint32_t)(e >> 32));  // past a multiple of 2^32
+  constexpr int U = kCodedQuads;
+  const int at = (threadIdx.x >> 6) * (256 * U) + (threadIdx.x & 63) * 4;
+  const auto process = [&](auto full) {
+    const auto valid = [&](int j) { return decltype(full)::value ? 4 : (int)s.count - (at + 256 * j); };
+    float th[U][4];
+    Raw4<G> gr[U];
+    uint32_t mw[U], vw[U], mb[U], vb[U];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      mm[c] = new_m(b1, r.c1, mm[c], gr[c]);
-      vv[c] = new_v(b2, r.c2, vv[c], gr[c]);
-      th[c] = new_theta(r, th[c], mm[c], vv[c]);
-      if (c >= n) mm[c] = vv[c] = 0.0f;  // not the tensor's: no part of the block's maximum
+    for (int j = 0; j < U; ++j) {
+      const int e = at + 256 * j;
+      const bool any = valid(j) > 0;
+      load4(theta + e, valid(j), th[j]);
+      gr[j].load(grad + e, valid(j));
+      mw[j] = load_codes(m + e, valid(j));
+      vw[j] = load_codes(v + e, valid(j));
+      mb[j] = any ? ms[e / kCodeBlock] : 0;
+      vb[j] = any ? vs[e / kCodeBlock] : 0;
     }
-    uint32_t mtop = block_largest(max4(magnitude(mm[0]), magnitude(mm[1]), magnitude(mm[2]), magnitude(mm[3])));
-    uint32_t vtop = block_largest(max4(magnitude(vv[0]), magnitude(vv[1]), magnitude(vv[2]), magnitude(vv[3])));
-    uint32_t mbad = 0, vbad = 0;
-    if (__any(max(mtop, vtop) >= kInfinity)) {  // some value is not finite: it becomes NaN, the maximum is the others'
-      mtop = block_largest(max4(finite_magnitude(mm[0]), finite_magnitude(mm[1]), finite_magnitude(mm[2]),
-                                finite_magnitude(mm[3])));
-      vtop = block_largest(max4(finite_magnitude(vv[0]), finite_magnitude(vv[1]), finite_magnitude(vv[2]),
-                                finite_magnitude(vv[3])));
+    const double clip = clip_of(a, i);
+    if (!takes_step(clip)) return;
+    const uint64_t t = next_step(a, i);
+    const Rates r = rates_of(a.group[g.group[s.range]], clip, a.lr_scale != nullptr ? a.lr_scale[i] : 1.0, t);
+    const Keys first = keys_of(a.seed, t, i, (uint32_t)(s.base >> 32));
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int at_j = at + 256 * j;
+      const int n = valid(j);
+      const uint32_t e = (uint32_t)s.base + at_j;
+      Keys k = first;
+      if (e < (uint32_t)s.base) k = keys_of(a.seed, t, i, (uint32_t)(s.base >> 32) + 1);  // past a multiple of 2^32
+      const double b1 = scaled(r.b1, mb[j]), b2 = scaled(r.b2, vb[j]);
+      float mm[4], vv[4];
+      decode_m(mw[j], mm);
+      decode_v(vw[j], vv);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        if (magnitude(mm[c]) >= kInfinity) mbad |= 0xFFu << (8 * c);
-        if (magnitude(vv[c]) >= kInfinity) vbad |= 0xFFu << (8 * c);
+        mm[c] = new_m(b1, r.c1, mm[c], gr[j].value(c));
+        vv[c] = new_v(b2, r.c2, vv[c], gr[j].value(c));
+        th[j][c] = new_theta(r, th[j][c], mm[c], vv[c]);
+        if (c >= n) mm[c] = vv[c] = 0.0f;  // not the tensor's: no part of the block's maximum
       }
-    }
-    const uint32_t mb = scale_byte(mtop, kTopM), vb = scale_byte(vtop, kTopV);
-    const float mi = inverse_scale(mb), vi = inverse_scale(vb);
-    float vy[4];
+      // every lane of a step takes part in its block's maximum
+      uint32_t mtop = block_largest(max4(magnitude(mm[0]), magnitude(mm[1]), magnitude(mm[2]), magnitude(mm[3])));
+      uint32_t vtop = block_largest(max4(magnitude(vv[0]), magnitude(vv[1]), magnitude(vv[2]), magnitude(vv[3])));
+      uint32_t mbad = 0, vbad = 0;
+      if (__any(max(mtop, vtop) >= kInfinity)) {  // some value is not finite: it becomes NaN, the maximum is the others'
+        mtop = block_largest(max4(finite_magnitude(mm[0]), finite_magnitude(mm[1]), finite_magnitude(mm[2]),
+                                  finite_magnitude(mm[3])));
+        vtop = block_largest(max4(finite_magnitude(vv[0]), finite_magnitude(vv[1]), finite_magnitude(vv[2]),
+                                  finite_magnitude(vv[3])));
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float y = vv[c] * vi;
-      vy[c] = vv[c] > 0.0f && y < kLeastV ? kLeastV : y;  // a positive v is not coded as 0
+        for (int c = 0; c < 4; ++c) {
+          if (magnitude(mm[c]) >= kInfinity) mbad |= 0xFFu << (8 * c);
+          if (magnitude(vv[c]) >= kInfinity) vbad |= 0xFFu << (8 * c);
+        }
+      }
+      const uint32_t mbyte = scale_byte(mtop, kTopM), vbyte = scale_byte(vtop, kTopV);
+      const float mi = inverse_scale(mbyte), vi = inverse_scale(vbyte);
+      float vy[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float y = vv[c] * vi;
+        vy[c] = vv[c] > 0.0f && y < kLeastV ? kLeastV : y;  // a positive v is not coded as 0
+      }
+      uint32_t mcode = 0, vcode = 0;
+      const uint32_t w0 = random_bits(k, e), w1 = random_bits(k, e + 1), w2 = random_bits(k, e + 2);
+      const uint32_t w3 = random_bits(k, e + 3);
+      code_m<0>(mcode, mm[0] * mi, w0), code_v<0>(vcode, vy[0], w0);
+      code_m<1>(mcode, mm[1] * mi, w1), code_v<1>(vcode, vy[1], w1);
+      code_m<2>(mcode, mm[2] * mi, w2), code_v<2>(vcode, vy[2], w2);
+      code_m<3>(mcode, mm[3] * mi, w3), code_v<3>(vcode, vy[3], w3);
+      store4(theta + at_j, n, th[j]);
+      store_codes(m + at_j, n, (mcode & ~mbad) | (kNaNs & mbad));
+      store_codes(v + at_j, n, (vcode & ~vbad) | (kNaNs & vbad));
+      if (n > 0 && at_j % kCodeBlock == 0) {
+        ms[at_j / kCodeBlock] = (uint8_t)mbyte;
+        vs[at_j / kCodeBlock] = (uint8_t)vbyte;
+      }
+      if constexpr (!std::is_void_v<W>) store4((W*)a.working + row + at_j, n, th[j]);
     }
-    uint32_t mw = 0, vw = 0;
-    const uint32_t w0 = random_bits(k, (uint32_t)e), w1 = random_bits(k, (uint32_t)e + 1);
-    const uint32_t w2 = random_bits(k, (uint32_t)e + 2), w3 = random_bits(k, (uint32_t)e + 3);
-    code_m<0>(mw, mm[0] * mi, w0), code_v<0>(vw, vy[0], w0);
-    code_m<1>(mw, mm[1] * mi, w1), code_v<1>(vw, vy[1], w1);
-    code_m<2>(mw, mm[2] * mi, w2), code_v<2>(vw, vy[2], w2);
-    code_m<3>(mw, mm[3] * mi, w3), code_v<3>(vw, vy[3], w3);
-    store4(theta + e, n, th);
-    store_codes(m + e, n, (mw & ~mbad) | (kNaNs & mbad));
-    store_codes(v + e, n, (vw & ~vbad) | (kNaNs & vbad));
-    if (any && e % kCodeBlock == 0) {
-      ms[e / kCodeBlock] = (uint8_t)mb;
-      vs[e / kCodeBlock] = (uint8_t)vb;
-    }
-    if constexpr (!std::is_void_v<W>) store4((W*)a.working + row + e, n, th);
-  }
+  };
+  if (s.count == 4 * kAdamWBlock * U) process(std::true_type());
+  else process(std::false_type());
 }
 
 __global__ __launch_bounds__(64) void k_adamw_advance(const AdamWArgs a) {
   if ((int)threadIdx.x >= a.n_present) return;
   const int i = a.learner[threadIdx.x];
-  if (takes_step(clip_of(a, i))) a.steps[i] += 1;
+  if (takes_step(clip_of(a, i))) a.steps[i] = (a.steps[i] & (int64_t)(kTicket - 1)) + 1;
 }
 
 template <typename G, typename W>
 hipError_t launch_adamw_gw(const AdamWArgs& a, bool coded, const InnerGeom& g, hipStream_t s) {
-  const dim3 grid(g.n_blocks, a.n_present), block(kInnerBlock);
+  const dim3 grid(g.n_blocks, a.n_present), block(kAdamWBlock);
   if (coded) {
     hipLaunchKernelGGL((k_adamw_coded<G, W>), grid, block, 0, s, a, g);
   } else {
@@ -469,7 +595,7 @@ hipError_t launch_adamw_g(const AdamWArgs& a, int32_t working_type, bool coded, 
 }  // namespace
 
 hipError_t launch_norm_partial(const NormArgs& a, int32_t grad_type, const InnerGeom& g, hipStream_t s) {
-  const dim3 grid(g.n_blocks, a.n_present), block(kInnerBlock);
+  const dim3 grid(g.n_blocks, a.n_present), block(kNormBlock);
   switch (grad_type) {
     case kBF16: hipLaunchKernelGGL(k_norm_partial<__bf16>, grid, block, 0, s, a, g); break;
     case kF16: hipLaunchKernelGGL(k_norm_partial<_Float16>, grid, block, 0, s, a, g); break;
@@ -478,8 +604,18 @@ hipError_t launch_norm_partial(const NormArgs& a, int32_t grad_type, const Inner
   return hipGetLastError();
 }
 
+hipError_t launch_norm_small(const NormArgs& a, int32_t grad_type, const InnerGeom& g, hipStream_t s) {
+  const dim3 grid(a.n_present), block(kNormFinal);
+  switch (grad_type) {
+    case kBF16: hipLaunchKernelGGL(k_norm_small<__bf16>, grid, block, 0, s, a, g); break;
+    case kF16: hipLaunchKernelGGL(k_norm_small<_Float16>, grid, block, 0, s, a, g); break;
+    default: hipLaunchKernelGGL(k_norm_small<float>, grid, block, 0, s, a, g); break;
+  }
+  return hipGetLastError();
+}
+
 hipError_t launch_norm_final(const NormArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(k_norm_final, dim3(a.n_present), dim3(kInnerBlock), 0, s, a);
+  hipLaunchKernelGGL(k_norm_final, dim3(a.n_present), dim3(kNormFinal), 0, s, a);
   return hipGetLastError();
 }
 

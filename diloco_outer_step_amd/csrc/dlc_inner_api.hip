@@ -23,23 +23,24 @@ using dlc::ok;
 using dlc::round256;
 
 constexpr int64_t kNormBlocks = 2048;
-constexpr int64_t kAdamWTiles = 2;
+
+// A grid's x extent times its block must stay below 2^32 threads; a range has at most
+// 2^32 / 512 = 2^23 AdamW tiles.
+constexpr int64_t kMaxLaunchBlocks = int64_t(1) << 24;
 
 struct InnerPartition {
   std::vector<dlc::InnerGeom> launches;
   int64_t n_slots = 0;
 };
 
+struct Range {
+  int64_t lo, count;
+  int32_t group;
+};
+
 // Tensors of one group that follow each other in the row without padding become one
-// range (of at most 2^32 - 1 elements); every range gets ceil(tiles / tiles_per_block)
-// blocks, tiles_per_block at least min_tiles and such that the call has about
-// target_blocks blocks.
-InnerPartition inner_partition(const dlc_tensor* t, int32_t n, const int32_t* group_of, int64_t min_tiles,
-                               int64_t target_blocks) {
-  struct Range {
-    int64_t lo, count;
-    int32_t group;
-  };
+// range (of at most 2^32 - 1 elements).
+std::vector<Range> join_tensors(const dlc_tensor* t, int32_t n, const int32_t* group_of) {
   std::vector<Range> ranges;
   ranges.reserve(n);
   for (int32_t i = 0; i < n; ++i) {
@@ -53,38 +54,50 @@ InnerPartition inner_partition(const dlc_tensor* t, int32_t n, const int32_t* gr
     }
     ranges.push_back({t[i].loffset, t[i].numel, group});
   }
-  int64_t tiles = 0;
-  for (const Range& r : ranges) tiles += (r.count + dlc::kInnerTile - 1) / dlc::kInnerTile;
-  const int64_t tpb = std::max(min_tiles, (tiles + target_blocks - 1) / target_blocks);
+  return ranges;
+}
+
+// Launches of at most kMaxRanges ranges, one block for every per_block elements of a range.
+InnerPartition inner_partition(const std::vector<Range>& ranges, int64_t per_block) {
   InnerPartition p;
-  for (size_t s = 0; s < ranges.size(); s += dlc::kMaxRanges) {
-    dlc::InnerGeom g;
-    std::memset(&g, 0, sizeof(g));
-    g.n_ranges = (int32_t)std::min<size_t>(dlc::kMaxRanges, ranges.size() - s);
-    g.tiles_per_block = (int32_t)tpb;
-    g.slot_base = (int32_t)p.n_slots;
-    int64_t blocks = 0;
-    for (int32_t i = 0; i < g.n_ranges; ++i) {
-      const Range& r = ranges[s + i];
-      g.r[i] = {(uint32_t)(r.lo / DLC_ALIGN_ELEMS), (uint32_t)r.count, (uint32_t)blocks};
-      g.group[i] = (uint8_t)r.group;
-      blocks += (r.count + tpb * dlc::kInnerTile - 1) / (tpb * dlc::kInnerTile);
+  for (const Range& r : ranges) {
+    const int64_t blocks = (r.count + per_block - 1) / per_block;
+    if (p.launches.empty() || p.launches.back().n_ranges == dlc::kMaxRanges ||
+        p.launches.back().n_blocks + blocks > kMaxLaunchBlocks) {
+      p.launches.emplace_back();
+      std::memset(&p.launches.back(), 0, sizeof(dlc::InnerGeom));
+      p.launches.back().per_block = per_block;
+      p.launches.back().slot_base = (int32_t)p.n_slots;
     }
-    g.n_blocks = (int32_t)blocks;
+    dlc::InnerGeom& g = p.launches.back();
+    g.r[g.n_ranges] = {(uint32_t)(r.lo / DLC_ALIGN_ELEMS), (uint32_t)r.count, (uint32_t)g.n_blocks};
+    g.group[g.n_ranges++] = (uint8_t)r.group;
+    g.n_blocks += (int32_t)blocks;
     p.n_slots += blocks;
-    p.launches.push_back(g);
   }
   return p;
 }
 
-InnerPartition norm_partition(const dlc_tensor* t, int32_t n) { return inner_partition(t, n, nullptr, 1, kNormBlocks); }
-
-// A grid's x extent times its block must stay below 2^32 threads.
-constexpr int64_t kAdamWMaxBlocks = int64_t(1) << 22;
-
-InnerPartition adamw_partition(const dlc_tensor* t, int32_t n, const int32_t* group_of) {
-  return inner_partition(t, n, group_of, kAdamWTiles, kAdamWMaxBlocks);
+int64_t total_elements(const std::vector<Range>& ranges) {
+  int64_t n = 0;
+  for (const Range& r : ranges) n += r.count;
+  return n;
 }
+
+InnerPartition norm_partition(const std::vector<Range>& ranges) {
+  const int64_t steps = (total_elements(ranges) + dlc::kNormStep - 1) / dlc::kNormStep;
+  return inner_partition(ranges, dlc::kNormStep * std::max<int64_t>(1, (steps + kNormBlocks - 1) / kNormBlocks));
+}
+
+// Few elements in few ranges: one block per learner does it all.
+constexpr int64_t kSmallNorm = 1 << 16, kSmallNormRanges = 8;
+
+bool small_norm(const std::vector<Range>& ranges) {
+  return (int64_t)ranges.size() <= kSmallNormRanges && total_elements(ranges) <= kSmallNorm;
+}
+
+// Calls of at most this many blocks per learner count the step in the AdamW kernel itself.
+constexpr int64_t kMaxTickets = 1024;
 
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
@@ -162,7 +175,7 @@ int32_t adamw_step(float* theta_learners, const void* grads, int32_t grad_type, 
       return fail(DLC_ERR_INVALID_ARGUMENT, "betas must be in [0, 1)");
     if (!(s.eps >= FLT_MIN && s.eps <= FLT_MAX))
       return fail(DLC_ERR_INVALID_ARGUMENT, "eps must be a normal positive fp32 number");
-    a.group[q] = {s.lr, s.beta1, s.beta2, s.eps, s.weight_decay};
+    a.group[q] = {s.lr, s.beta1, s.beta2, s.eps, s.weight_decay, std::log(s.beta1), std::log(s.beta2)};
   }
   if (group_of) {
     for (int32_t t = 0; t < n_tensors; ++t)
@@ -182,13 +195,17 @@ int32_t adamw_step(float* theta_learners, const void* grads, int32_t grad_type, 
   a.stride = learner_stride;
   a.seed = mo.seed;
   const hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  const InnerPartition p = adamw_partition(tensors, n_tensors, group_of);
+  const InnerPartition p = inner_partition(join_tensors(tensors, n_tensors, group_of),
+                                           4 * dlc::kAdamWBlock * (mo.coded ? dlc::kCodedQuads : dlc::kAdamWQuads));
+  if (p.n_slots <= kMaxTickets && p.launches.size() == 1) a.tickets = (int32_t)p.n_slots;
   for (const dlc::InnerGeom& g : p.launches) {
     const hipError_t e = dlc::launch_adamw(a, grad_type, working ? working_type : dlc::kNone, mo.coded, g, s);
     if (e != hipSuccess) return hip_fail(e, "AdamW kernel launch");
   }
-  const hipError_t e = dlc::launch_adamw_advance(a, s);
-  if (e != hipSuccess) return hip_fail(e, "step count kernel launch");
+  if (a.tickets == 0) {
+    const hipError_t e = dlc::launch_adamw_advance(a, s);
+    if (e != hipSuccess) return hip_fail(e, "step count kernel launch");
+  }
   return ok();
 }
 
@@ -204,7 +221,8 @@ int32_t dlc_grad_norm_workspace_bytes(int32_t n_learners, const dlc_tensor* tens
       return fail(DLC_ERR_INVALID_ARGUMENT, "n_learners must be in [1, 64]");
     const int32_t rc = check_tensors(tensors, n_tensors, 0, false);
     if (rc != DLC_OK) return rc;
-    *bytes = round256((size_t)norm_partition(tensors, n_tensors).n_slots * n_learners * sizeof(double));
+    const InnerPartition p = norm_partition(join_tensors(tensors, n_tensors, nullptr));
+    *bytes = round256((size_t)p.n_slots * n_learners * sizeof(double));
     return ok();
   });
 }
@@ -231,7 +249,8 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
     if (!(std::isfinite(unscale) && unscale > 0.0))
       return fail(DLC_ERR_INVALID_ARGUMENT, "unscale must be finite and > 0");
     if (!(max_norm > 0.0)) return fail(DLC_ERR_INVALID_ARGUMENT, "max_norm must be > 0");
-    const InnerPartition p = norm_partition(tensors, n_tensors);
+    const std::vector<Range> ranges = join_tensors(tensors, n_tensors, nullptr);
+    const InnerPartition p = norm_partition(ranges);
     const size_t need = round256((size_t)p.n_slots * a.n_present * sizeof(double));
     if (workspace == nullptr || workspace_bytes < need)
       return fail(DLC_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
@@ -245,6 +264,10 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
     a.max_norm = max_norm;
     a.n_slots = (int32_t)p.n_slots;
     const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    if (small_norm(ranges)) {
+      const hipError_t e = dlc::launch_norm_small(a, grad_type, p.launches[0], s);
+      return e != hipSuccess ? hip_fail(e, "gradient norm kernel launch") : ok();
+    }
     for (const dlc::InnerGeom& g : p.launches) {
       const hipError_t e = dlc::launch_norm_partial(a, grad_type, g, s);
       if (e != hipSuccess) return hip_fail(e, "gradient norm kernel launch");
