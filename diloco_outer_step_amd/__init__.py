@@ -650,7 +650,7 @@ def _check_buffers(bufs):
     tests first, the naming checks only where it fails."""
     dev = bufs[0][1].get_device()
     for _, t, dtype, shape in bufs:
-        if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_contiguous()
+        if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
                 or t.get_device() != dev or dev < 0):
             break
     else:
@@ -672,26 +672,28 @@ def _row_shape(t, tensors, name: str) -> Tuple[int, int]:
     return t.shape
 
 
-class _OnDevice:
-    """The buffers' device made current for the call where it is not, and the handle of the
-    stream on it: the caller's, or that device's current one."""
-
-    def __init__(self, index: int, stream):
+def _on_device(index: int, stream, fn, *args) -> None:
+    """fn(*args, stream handle) with the buffers' device current: on the caller's stream, or
+    on that device's current one."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
         if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
             raise ValueError(f"the stream is on {stream.device}, the call's buffers on cuda:{index}")
-        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
-        self.index, self.stream = index, stream
+        handle = _stream(stream)
+    if index == torch.cuda.current_device():
+        _check(fn(*args, handle))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, handle))
 
-    def __enter__(self) -> int:
-        if self.guard is not None:
-            self.guard.__enter__()
-        if self.stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.index)
-        return _stream(self.stream).value or 0
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _presence(present, k):
+    """Presence list for the C ABI: NULL where every learner is present."""
+    if present is None:
+        return None
+    _present_list(present, k)
+    return None if all(present) else (ctypes.c_uint8 * k)(*[1 if p else 0 for p in present])
 
 
 def _address(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -722,17 +724,16 @@ def dlc_grad_norm(grads, tensors, norm, grad_scale, workspace, max_norm=float("i
     finite); both device fp64 [K].  grads: [K, learner_stride] fp32, bf16 or fp16."""
     k, stride = _row_shape(grads, tensors, "grads")
     gt = _float_type(grads, "grads", _FLOAT_TYPES)
-    _present_list(present, k)
+    pres = _presence(present, k)
     if not isinstance(workspace, torch.Tensor):
         raise TypeError(f"workspace must be a torch.Tensor, not {type(workspace).__name__}")
     _check_buffers((("grads", grads, grads.dtype, (k, stride)), ("norm", norm, torch.float64, (k,)),
                     ("grad_scale", grad_scale, torch.float64, (k,)),
                     ("workspace", workspace, torch.uint8, workspace.shape)))
     arr, n = _tensors(tensors)
-    _buf, pres = _present(present, k)
-    with _OnDevice(grads.get_device(), stream) as s:
-        _check(_lib.dlc_grad_norm(grads.data_ptr(), gt, stride, k, pres, arr, n, float(unscale), float(max_norm),
-                                  norm.data_ptr(), grad_scale.data_ptr(), workspace.data_ptr(), workspace.numel(), s))
+    _on_device(grads.get_device(), stream, _lib.dlc_grad_norm, grads.data_ptr(), gt, stride, k, pres, arr, n,
+               float(unscale), float(max_norm), norm.data_ptr(), grad_scale.data_ptr(), workspace.data_ptr(),
+               workspace.numel())
 
 
 def coded_moments(n_learners: int, learner_stride: int, device="cuda"):
@@ -750,7 +751,7 @@ def _adamw(theta_L, grads, moments, steps, tensors, groups, group_of, grad_scale
     """Buffer checks of an AdamW call -> the arguments its two forms share.  moments:
     (name, tensor, dtype, elements per value) each."""
     k, stride = _row_shape(theta_L, tensors, "theta_L")
-    _present_list(present, k)
+    pres = _presence(present, k)
     gt, wt = _float_type(grads, "grads", _FLOAT_TYPES), DLC_FLOAT32
     rows, per_learner = (k, stride), (k,)
     bufs = [("theta_L", theta_L, torch.float32, rows), ("grads", grads, grads.dtype, rows),
@@ -774,10 +775,12 @@ def _adamw(theta_L, grads, moments, steps, tensors, groups, group_of, grad_scale
             raise ValueError(f"group_of holds {ids.size} values for {len(tensors)} tensors")
     _check_buffers(bufs)
     arr, n = _tensors(tensors)
-    buf, pres = _present(present, k)
-    keep = (buf, ids)  # alive until the call returns
-    return (gt, stride, k, pres, arr, n, None if ids is None else ids.ctypes.data, gs, len(groups),
-            _address(grad_scale), _address(lr_scale), _address(working), wt, keep)
+    return (gt, stride, k, pres, arr, n, ids, gs, len(groups), _address(grad_scale), _address(lr_scale),
+            _address(working), wt)
+
+
+def _ids_address(ids) -> Optional[int]:
+    return None if ids is None else ids.__array_interface__["data"][0]
 
 
 def dlc_adamw_step(theta_L, grads, exp_avg, exp_avg_sq, steps, tensors, groups=AdamWGroup(), group_of=None,
@@ -788,12 +791,12 @@ def dlc_adamw_step(theta_L, grads, exp_avg, exp_avg_sq, steps, tensors, groups=A
     tensor's; grad_scale, lr_scale: device fp64 [K] (a learner whose grad_scale is not
     finite and positive is left out); working: bf16 or fp16 [K, learner_stride], the
     updated parameters rounded."""
-    gt, stride, k, pres, arr, n, ids, gs, ng, scale, lrs, work, wt, _keep = _adamw(
+    gt, stride, k, pres, arr, n, ids, gs, ng, scale, lrs, work, wt = _adamw(
         theta_L, grads, (("exp_avg", exp_avg, torch.float32, 1), ("exp_avg_sq", exp_avg_sq, torch.float32, 1)), steps,
         tensors, groups, group_of, grad_scale, lr_scale, working, present)
-    with _OnDevice(theta_L.get_device(), stream) as s:
-        _check(_lib.dlc_adamw_step(theta_L.data_ptr(), grads.data_ptr(), gt, exp_avg.data_ptr(), exp_avg_sq.data_ptr(),
-                                   steps.data_ptr(), stride, k, pres, arr, n, ids, gs, ng, scale, lrs, work, wt, s))
+    _on_device(theta_L.get_device(), stream, _lib.dlc_adamw_step, theta_L.data_ptr(), grads.data_ptr(), gt,
+               exp_avg.data_ptr(), exp_avg_sq.data_ptr(), steps.data_ptr(), stride, k, pres, arr, n, _ids_address(ids),
+               gs, ng, scale, lrs, work, wt)
 
 
 def dlc_adamw_coded_step(theta_L, grads, m_codes, m_scales, v_codes, v_scales, steps, tensors, groups=AdamWGroup(),
@@ -804,13 +807,11 @@ def dlc_adamw_coded_step(theta_L, grads, m_codes, m_scales, v_codes, v_scales, s
     [K, learner_stride / 64].  seed: of the stochastic rounding, 0 <= seed < 2^64."""
     if not 0 <= int(seed) < 1 << 64:
         raise ValueError("seed must be in [0, 2^64)")
-    gt, stride, k, pres, arr, n, ids, gs, ng, scale, lrs, work, wt, _keep = _adamw(
+    gt, stride, k, pres, arr, n, ids, gs, ng, scale, lrs, work, wt = _adamw(
         theta_L, grads,
         (("m_codes", m_codes, torch.float8_e4m3fn, 1), ("m_scales", m_scales, torch.uint8, DLC_CODE_BLOCK),
          ("v_codes", v_codes, torch.float8_e5m2, 1), ("v_scales", v_scales, torch.uint8, DLC_CODE_BLOCK)),
         steps, tensors, groups, group_of, grad_scale, lr_scale, working, present)
-    with _OnDevice(theta_L.get_device(), stream) as s:
-        _check(_lib.dlc_adamw_coded_step(theta_L.data_ptr(), grads.data_ptr(), gt, m_codes.data_ptr(),
-                                         m_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-                                         steps.data_ptr(), stride, k, pres, arr, n, ids, gs, ng, int(seed), scale, lrs,
-                                         work, wt, s))
+    _on_device(theta_L.get_device(), stream, _lib.dlc_adamw_coded_step, theta_L.data_ptr(), grads.data_ptr(), gt,
+               m_codes.data_ptr(), m_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), steps.data_ptr(),
+               stride, k, pres, arr, n, _ids_address(ids), gs, ng, int(seed), scale, lrs, work, wt)

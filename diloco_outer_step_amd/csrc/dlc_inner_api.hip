@@ -96,8 +96,11 @@ bool small_norm(const std::vector<Range>& ranges) {
   return (int64_t)ranges.size() <= kSmallNormRanges && total_elements(ranges) <= kSmallNorm;
 }
 
-// Calls of at most this many blocks per learner count the step in the AdamW kernel itself.
-constexpr int64_t kMaxTickets = 1024;
+// Calls of at most this many blocks per learner count the step in the AdamW kernel itself:
+// one launch less is 2.7 us less where the host's launches are the time (11.4 against
+// 14.1 us for four vectors, 32 blocks), but tickets on one address pass at about 45 ns
+// each (9100 of them: 431 us for a call that takes 31).
+constexpr int64_t kMaxTickets = 32;
 
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
