@@ -14,14 +14,27 @@
 
 namespace dlc {
 
-constexpr int kMaxRanges = 216;
+constexpr int kMaxRanges = 208;
+constexpr int kRangeBuckets = 64;
 constexpr int kMaxGroups = 16;
 constexpr int kCodeBlock = 64;       // elements that share a scale byte
-// AdamW: a block takes one tile, its threads kAdamWQuads (kCodedQuads) times four elements each.
-constexpr int kAdamWBlock = 128;
-constexpr int kAdamWQuads = 1;
+// AdamW with 32-bit moments: one wave takes 256 elements, four a thread, and is done.  The
+// LDS that a block asks for and does not use keeps 11 of them on a CU: what the device then
+// works on at a time is a shorter stretch of each of the arrays, and memory serves it
+// faster.  1B set, bf16 gradients and working copy, on one machine: 11 blocks a CU 3.62 ms
+// (6.6 TB/s), 9: 3.82, 14: 3.72, 20: 3.89, no bound: 4.02; with blocks of 128 threads and 14 waves a
+// CU 3.76; runs of 8192 elements per block 4.55, a persistent grid 4.81 and more.
+constexpr int kAdamWBlock = 64;
+constexpr int kAdamWTile = 4 * kAdamWBlock;
+constexpr int kAdamWLds = 14800;
+// With coded moments: two waves, eight elements a thread (twice the arithmetic per byte, and
+// loads of 4 bytes: one quad a thread was 8% slower); its registers already leave 20 waves a CU.
+constexpr int kCodedBlock = 128;
 constexpr int kCodedQuads = 2;
-// Gradient norm: a block takes whole steps of kNormBlock threads times kNormLoads 16-byte loads.
+constexpr int kCodedTile = 4 * kCodedBlock * kCodedQuads;
+// Gradient norm: about kNormBlocks blocks a launch, each with its own run of whole steps of
+// kNormBlock threads times kNormLoads 16-byte loads (half or twice the loads and 1024 to
+// 16384 blocks are within 4%; steps dealt out in turn are 2% slower).
 constexpr int kNormBlock = 256;
 constexpr int kNormLoads = 4;
 constexpr int kNormStep = kNormBlock * kNormLoads * 4;  // elements, fp32
@@ -29,19 +42,31 @@ constexpr int kNormFinal = 1024;     // threads of the final sum
 
 enum FloatType : int32_t { kF32 = 0, kBF16 = 1, kF16 = 2, kNone = -1 };
 
+constexpr int kGroupShift = 28;  // blocks of a launch stay below 2^28
+
 struct InnerRange {
   uint32_t lo64;         // first element of the row, in units of 64
   uint32_t count;        // elements
-  uint32_t block_first;  // first block of this range within the launch
+  uint32_t first_group;  // first block of this range within the launch, and its group << kGroupShift
+  __host__ __device__ uint32_t block_first() const { return first_group & ((1u << kGroupShift) - 1); }
+  __host__ __device__ uint32_t group() const { return first_group >> kGroupShift; }
 };
 
 struct InnerGeom {
   int32_t n_ranges;
   int32_t n_blocks;
-  int64_t per_block;     // elements per block
+  uint32_t per_block;    // elements per block
   int32_t slot_base;     // the launch's first slot of block partials
+  int32_t bucket_shift;  // blocks [k << shift, (k + 1) << shift) lie in ranges first .. last of bucket k
+  uint32_t bucket[kRangeBuckets];  // first | last << 16
   InnerRange r[kMaxRanges];
-  uint8_t group[kMaxRanges];
+};
+
+// Present position -> learner, four to a word: the kernels read words (a byte would be a
+// vector load).
+struct LearnerList {
+  uint32_t word[16];
+  __host__ __device__ int operator[](uint32_t k) const { return (int)(word[k >> 2] >> (8 * (k & 3)) & 0xFFu); }
 };
 
 struct InnerGroup {
@@ -64,7 +89,7 @@ struct AdamWArgs {
   uint64_t seed;
   int32_t n_present;
   int32_t tickets;            // blocks per learner where the kernel counts the step itself, else 0
-  uint8_t learner[64];        // present position -> learner
+  LearnerList learner;
   InnerGroup group[kMaxGroups];
 };
 
@@ -77,7 +102,7 @@ struct NormArgs {
   double unscale, max_norm;
   int32_t n_present;
   int32_t n_slots;
-  uint8_t learner[64];
+  LearnerList learner;
 };
 
 // HIP passes at most 4 KB of kernel arguments.

@@ -31,27 +31,29 @@ namespace {
 typedef float vf4 __attribute__((ext_vector_type(4)));
 typedef unsigned int vu2 __attribute__((ext_vector_type(2)));
 
-// Block -> (range, first element of the row, elements).  The launch geometry lives in the
-// kernel arguments; the search index is uniform across the block (scalar loads).
+// Block -> (group, first element of the row, elements).  The launch geometry lives in the
+// kernel arguments and is read by scalar loads; the bucket of the block number leaves few
+// ranges, mostly one, to search.
 struct Spot {
-  int range;
+  int group;
   int64_t base;
-  int64_t count;
+  uint32_t count;
 };
 
-__device__ __forceinline__ Spot spot(const InnerGeom& g) {
+__device__ __forceinline__ Spot spot(const InnerGeom& g, uint32_t per_block) {
   const uint32_t b = blockIdx.x;
-  int lo = 0, hi = g.n_ranges - 1;
+  const uint32_t bucket = g.bucket[b >> g.bucket_shift];
+  int lo = (int)(bucket & 0xFFFFu), hi = (int)(bucket >> 16);
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (g.r[mid].block_first <= b) lo = mid; else hi = mid - 1;
+    if (g.r[mid].block_first() <= b) lo = mid; else hi = mid - 1;
   }
   const InnerRange r = g.r[lo];
-  const int64_t first = (int64_t)(b - r.block_first) * g.per_block;
+  const uint32_t first = (b - r.block_first()) * per_block;  // below count, so below 2^32
   Spot s;
-  s.range = lo;
+  s.group = (int)r.group();
   s.base = (int64_t)r.lo64 * 64 + first;
-  s.count = (int64_t)r.count - first < g.per_block ? (int64_t)r.count - first : g.per_block;
+  s.count = r.count - first < per_block ? r.count - first : per_block;
   return s;
 }
 
@@ -188,7 +190,7 @@ __device__ __forceinline__ void write_norm(const NormArgs& a, int i, double sum)
 
 template <typename G>
 __global__ __launch_bounds__(kNormBlock) void k_norm_partial(const NormArgs a, const InnerGeom g) {
-  const Spot sp = spot(g);
+  const Spot sp = spot(g, g.per_block);
   const G* row = (const G*)a.grads + (int64_t)a.learner[blockIdx.y] * a.stride;
   const double s = block_sum<kNormBlock>(squares<kNormBlock, kNormLoads>(row + sp.base, sp.count));
   if (threadIdx.x == 0) a.part[(size_t)blockIdx.y * a.n_slots + g.slot_base + blockIdx.x] = s;
@@ -260,8 +262,10 @@ __device__ __forceinline__ Rates rates_of(const InnerGroup& q, double clip, doub
   r.b2 = q.beta2;
   r.c2 = (1.0 - q.beta2) * clip * clip;
   r.shrink = (float)(eta * q.weight_decay);
-  r.size = (float)eta * __builtin_amdgcn_rcpf((float)one_minus_exp((double)t * q.log_beta1));
-  r.root = __builtin_amdgcn_rsqf((float)one_minus_exp((double)t * q.log_beta2));
+  // both corrections in one evaluation: beta1 in the even lanes, beta2 in the odd ones
+  const int c = __float_as_int((float)one_minus_exp((double)t * (threadIdx.x & 1 ? q.log_beta2 : q.log_beta1)));
+  r.size = (float)eta * __builtin_amdgcn_rcpf(__int_as_float(__builtin_amdgcn_readlane(c, 0)));
+  r.root = __builtin_amdgcn_rsqf(__int_as_float(__builtin_amdgcn_readlane(c, 1)));
   r.eps = (float)q.eps;
   return r;
 }
@@ -277,13 +281,31 @@ __device__ __forceinline__ float new_v(double b2, double c2, double v, double gr
   return (float)(b2 * v + c2 * grad * grad);
 }
 
+// What a block reads of its learner, before its tile: the loads overlap the search for the
+// block's range.
+struct Learner {
+  double clip, lr_scale;
+  uint64_t steps;
+};
+
+__device__ __forceinline__ Learner learner_of(const AdamWArgs& a, int i) {
+  // no branches: an absent array's place is taken by steps, whose bits are not used
+  const double* clip = a.grad_scale != nullptr ? a.grad_scale : (const double*)a.steps;
+  const double* lr = a.lr_scale != nullptr ? a.lr_scale : (const double*)a.steps;
+  const double c = clip[i], s = lr[i];
+  Learner l;
+  l.steps = (uint64_t)a.steps[i];
+  l.clip = a.grad_scale != nullptr ? c : 1.0;
+  l.lr_scale = a.lr_scale != nullptr ? s : 1.0;
+  return l;
+}
+
 // The learner's step number t = steps + 1.  In calls of few blocks the blocks themselves
 // count the step: each adds a ticket above the count once all of its threads have read
 // it, and the one that draws the last ticket writes t over count and tickets.
-__device__ __forceinline__ uint64_t next_step(const AdamWArgs& a, int i) {
-  const uint64_t steps = (uint64_t)a.steps[i];
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)steps);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(steps >> 32));
+__device__ __forceinline__ uint64_t next_step(const AdamWArgs& a, int i, const Learner& l) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)l.steps);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(l.steps >> 32));
   const uint64_t t = (((uint64_t)hi << 32 | lo) & (kTicket - 1)) + 1;
   if (a.tickets != 0) {
     asm volatile("" : : "s"(lo), "s"(hi) : "memory");  // the count has arrived before the barrier
@@ -298,60 +320,60 @@ __device__ __forceinline__ uint64_t next_step(const AdamWArgs& a, int i) {
 }
 
 // theta - (eta wd theta + step).  The hardware's square root and reciprocal are within
-// one unit in the last place but take no subnormal operand: a tiny v is scaled up (eps,
-// and with it the denominator, is a normal number).  m may be subnormal, so it is
-// divided before it is scaled.
+// one unit in the last place but take no subnormal operand: kTinyV scales a tiny v up.
+// m may be subnormal, so it is divided before it is scaled.
+template <bool kTinyV>
 __device__ __forceinline__ float new_theta(const Rates& r, float theta, float m, float v) {
-  const bool tiny = v < 0x1p-96f;
-  const float s = __builtin_amdgcn_sqrtf(tiny ? v * 0x1p64f : v) * (tiny ? 0x1p-32f : 1.0f);
+  const bool tiny = kTinyV && v < 0x1p-96f;
+  float s = __builtin_amdgcn_sqrtf(tiny ? v * 0x1p64f : v);
+  if (kTinyV) s *= tiny ? 0x1p-32f : 1.0f;
   const float q = m * __builtin_amdgcn_rcpf(__fmaf_rn(s, r.root, r.eps));
   return theta - __fmaf_rn(r.shrink, theta, r.size * q);
 }
 
+// A subnormal v taken as 0 changes the denominator by less than 2^-63 root: nothing next
+// to an eps of 2^-40 root (9e-13 of it; eps is 1e-8 by default, root 32 at the most).
+__device__ __forceinline__ bool tiny_v_matters(const Rates& r) { return r.eps < r.root * 0x1p-40f; }
+
 template <typename G, typename W>
 __global__ __launch_bounds__(kAdamWBlock) void k_adamw(const AdamWArgs a, const InnerGeom g) {
-  constexpr int U = kAdamWQuads;
-  const Spot s = spot(g);
   const int i = a.learner[blockIdx.y];
+  const Learner l = learner_of(a, i);
+  const Spot s = spot(g, kAdamWTile);
   const int64_t row = (int64_t)i * a.stride + s.base;
   float* theta = a.theta + row;
   float* m = (float*)a.m + row;
   float* v = (float*)a.v + row;
   const G* grad = (const G*)a.grads + row;
-  float th[U][4], mm[U][4], vv[U][4];
-  Raw4<G> gr[U];
-  const int at = (threadIdx.x >> 6) * (256 * U) + (threadIdx.x & 63) * 4;
-  const auto process = [&](auto full) {
-    const auto valid = [&](int j) { return decltype(full)::value ? 4 : (int)s.count - (at + 256 * j); };
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int e = at + 256 * j;
-      load4(theta + e, valid(j), th[j]);
-      load4(m + e, valid(j), mm[j]);
-      load4(v + e, valid(j), vv[j]);
-      gr[j].load(grad + e, valid(j));
-    }
-    const double clip = clip_of(a, i);
-    if (!takes_step(clip)) return;
-    const uint64_t t = next_step(a, i);
-    const Rates r = rates_of(a.group[g.group[s.range]], clip, a.lr_scale != nullptr ? a.lr_scale[i] : 1.0, t);
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int e = at + 256 * j;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        mm[j][c] = new_m(r.b1, r.c1, mm[j][c], gr[j].value(c));
-        vv[j][c] = new_v(r.b2, r.c2, vv[j][c], gr[j].value(c));
-        th[j][c] = new_theta(r, th[j][c], mm[j][c], vv[j][c]);
-      }
-      store4(theta + e, valid(j), th[j]);
-      store4(m + e, valid(j), mm[j]);
-      store4(v + e, valid(j), vv[j]);
-      if constexpr (!std::is_void_v<W>) store4((W*)a.working + row + e, valid(j), th[j]);
-    }
+  const int at = threadIdx.x * 4;
+  const int n = (int)s.count - at;
+  const bool full = s.count == kAdamWTile;
+  float th[4], mm[4], vv[4];
+  Raw4<G> gr;
+  const auto load = [&](int n) {
+    load4(theta + at, n, th);
+    load4(m + at, n, mm);
+    load4(v + at, n, vv);
+    gr.load(grad + at, n);
   };
-  if (s.count == 4 * kAdamWBlock * U) process(std::true_type());
-  else process(std::false_type());
+  if (full) load(4);
+  else load(n);
+  if (!takes_step(l.clip)) return;
+  const Rates r = rates_of(a.group[s.group], l.clip, l.lr_scale, next_step(a, i, l));
+  const auto finish = [&](auto fast, int n) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      mm[c] = new_m(r.b1, r.c1, mm[c], gr.value(c));
+      vv[c] = new_v(r.b2, r.c2, vv[c], gr.value(c));
+      th[c] = new_theta<!decltype(fast)::value>(r, th[c], mm[c], vv[c]);
+    }
+    store4(theta + at, n, th);
+    store4(m + at, n, mm);
+    store4(v + at, n, vv);
+    if constexpr (!std::is_void_v<W>) store4((W*)a.working + row + at, n, th);
+  };
+  if (full && !tiny_v_matters(r)) finish(std::true_type(), 4);
+  else finish(std::false_type(), n);
 }
 
 // --- coded moments -----------------------------------------------------------
@@ -387,7 +409,6 @@ __device__ __forceinline__ uint32_t random_bits(const Keys& k, uint32_t e) {
 // 448) or 2^14 (e5m2, 57344), so that no value reaches the format's end, rounded up or not.
 constexpr int kTopM = 7, kTopV = 14;
 constexpr uint32_t kNaNs = 0x7F7F7F7Fu;  // four NaNs of either format
-constexpr float kLeastV = 0x1p-16f;  // the smallest e5m2 number
 
 __device__ __forceinline__ uint32_t scale_byte(uint32_t largest, int top) {
   const int b = (int)(largest >> 23) - top;
@@ -471,9 +492,10 @@ __device__ __forceinline__ uint32_t max4(uint32_t a, uint32_t b, uint32_t c, uin
 }
 
 template <typename G, typename W>
-__global__ __launch_bounds__(kAdamWBlock) void k_adamw_coded(const AdamWArgs a, const InnerGeom g) {
-  const Spot s = spot(g);
+__global__ __launch_bounds__(kCodedBlock) void k_adamw_coded(const AdamWArgs a, const InnerGeom g) {
   const int i = a.learner[blockIdx.y];
+  const Learner l = learner_of(a, i);
+  const Spot s = spot(g, kCodedTile);
   const int64_t row = (int64_t)i * a.stride + s.base;
   float* theta = a.theta + row;
   uint8_t* m = (uint8_t*)a.m + row;
@@ -482,35 +504,40 @@ __global__ __launch_bounds__(kAdamWBlock) void k_adamw_coded(const AdamWArgs a, 
   uint8_t* vs = a.v_scale + row / kCodeBlock;
   const G* grad = (const G*)a.grads + row;
   constexpr int U = kCodedQuads;
-  const int at = (threadIdx.x >> 6) * (256 * U) + (threadIdx.x & 63) * 4;
-  const auto process = [&](auto full) {
-    const auto valid = [&](int j) { return decltype(full)::value ? 4 : (int)s.count - (at + 256 * j); };
-    float th[U][4];
-    Raw4<G> gr[U];
-    uint32_t mw[U], vw[U], mb[U], vb[U];
+  const int at = (threadIdx.x >> 6) * (256 * U) + (threadIdx.x & 63) * 4;  // quad j at + 256 j
+  const bool full = s.count == kCodedTile;
+  float th[U][4];
+  Raw4<G> gr[U];
+  uint32_t mw[U], vw[U], mb[U], vb[U];
+  const auto load = [&](auto whole) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int e = at + 256 * j;
-      const bool any = valid(j) > 0;
-      load4(theta + e, valid(j), th[j]);
-      gr[j].load(grad + e, valid(j));
-      mw[j] = load_codes(m + e, valid(j));
-      vw[j] = load_codes(v + e, valid(j));
-      mb[j] = any ? ms[e / kCodeBlock] : 0;
-      vb[j] = any ? vs[e / kCodeBlock] : 0;
+      const int n = decltype(whole)::value ? 4 : (int)s.count - e;
+      load4(theta + e, n, th[j]);
+      gr[j].load(grad + e, n);
+      mw[j] = load_codes(m + e, n);
+      vw[j] = load_codes(v + e, n);
+      mb[j] = n > 0 ? ms[e / kCodeBlock] : 0;
+      vb[j] = n > 0 ? vs[e / kCodeBlock] : 0;
     }
-    const double clip = clip_of(a, i);
-    if (!takes_step(clip)) return;
-    const uint64_t t = next_step(a, i);
-    const Rates r = rates_of(a.group[g.group[s.range]], clip, a.lr_scale != nullptr ? a.lr_scale[i] : 1.0, t);
-    const Keys first = keys_of(a.seed, t, i, (uint32_t)(s.base >> 32));
+  };
+  if (full) load(std::true_type());
+  else load(std::false_type());
+  if (!takes_step(l.clip)) return;
+  const uint64_t t = next_step(a, i, l);
+  const Rates r = rates_of(a.group[s.group], l.clip, l.lr_scale, t);
+  const Keys first = keys_of(a.seed, t, i, (uint32_t)(s.base >> 32));
+  const auto finish = [&](auto fast) {
+    constexpr bool kFast = decltype(fast)::value;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int at_j = at + 256 * j;
-      const int n = valid(j);
-      const uint32_t e = (uint32_t)s.base + at_j;
+      const int e = at + 256 * j;
+      const int n = kFast ? 4 : (int)s.count - e;
+      const uint32_t place = (uint32_t)s.base + e;
       Keys k = first;
-      if (e < (uint32_t)s.base) k = keys_of(a.seed, t, i, (uint32_t)(s.base >> 32) + 1);  // past a multiple of 2^32
+      if (!kFast && place < (uint32_t)s.base)  // past a multiple of 2^32
+        k = keys_of(a.seed, t, i, (uint32_t)(s.base >> 32) + 1);
       const double b1 = scaled(r.b1, mb[j]), b2 = scaled(r.b2, vb[j]);
       float mm[4], vv[4];
       decode_m(mw[j], mm);
@@ -519,7 +546,7 @@ __global__ __launch_bounds__(kAdamWBlock) void k_adamw_coded(const AdamWArgs a, 
       for (int c = 0; c < 4; ++c) {
         mm[c] = new_m(b1, r.c1, mm[c], gr[j].value(c));
         vv[c] = new_v(b2, r.c2, vv[c], gr[j].value(c));
-        th[j][c] = new_theta(r, th[j][c], mm[c], vv[c]);
+        th[j][c] = new_theta<!kFast>(r, th[j][c], mm[c], vv[c]);
         if (c >= n) mm[c] = vv[c] = 0.0f;  // not the tensor's: no part of the block's maximum
       }
       // every lane of a step takes part in its block's maximum
@@ -539,31 +566,32 @@ __global__ __launch_bounds__(kAdamWBlock) void k_adamw_coded(const AdamWArgs a, 
       }
       const uint32_t mbyte = scale_byte(mtop, kTopM), vbyte = scale_byte(vtop, kTopV);
       const float mi = inverse_scale(mbyte), vi = inverse_scale(vbyte);
-      float vy[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float y = vv[c] * vi;
-        vy[c] = vv[c] > 0.0f && y < kLeastV ? kLeastV : y;  // a positive v is not coded as 0
-      }
       uint32_t mcode = 0, vcode = 0;
-      const uint32_t w0 = random_bits(k, e), w1 = random_bits(k, e + 1), w2 = random_bits(k, e + 2);
-      const uint32_t w3 = random_bits(k, e + 3);
-      code_m<0>(mcode, mm[0] * mi, w0), code_v<0>(vcode, vy[0], w0);
-      code_m<1>(mcode, mm[1] * mi, w1), code_v<1>(vcode, vy[1], w1);
-      code_m<2>(mcode, mm[2] * mi, w2), code_v<2>(vcode, vy[2], w2);
-      code_m<3>(mcode, mm[3] * mi, w3), code_v<3>(vcode, vy[3], w3);
-      store4(theta + at_j, n, th[j]);
-      store_codes(m + at_j, n, (mcode & ~mbad) | (kNaNs & mbad));
-      store_codes(v + at_j, n, (vcode & ~vbad) | (kNaNs & vbad));
-      if (n > 0 && at_j % kCodeBlock == 0) {
-        ms[at_j / kCodeBlock] = (uint8_t)mbyte;
-        vs[at_j / kCodeBlock] = (uint8_t)vbyte;
+      const uint32_t w0 = random_bits(k, place), w1 = random_bits(k, place + 1), w2 = random_bits(k, place + 2);
+      const uint32_t w3 = random_bits(k, place + 3);
+      code_m<0>(mcode, mm[0] * mi, w0), code_v<0>(vcode, vv[0] * vi, w0);
+      code_m<1>(mcode, mm[1] * mi, w1), code_v<1>(vcode, vv[1] * vi, w1);
+      code_m<2>(mcode, mm[2] * mi, w2), code_v<2>(vcode, vv[2] * vi, w2);
+      code_m<3>(mcode, mm[3] * mi, w3), code_v<3>(vcode, vv[3] * vi, w3);
+      if (__any(((vcode - 0x01010101u) & ~vcode & 0x80808080u) != 0)) {  // a byte is 0: not for a positive v
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if ((vcode >> (8 * c) & 0xFFu) == 0 && vv[c] > 0.0f) vcode |= 1u << (8 * c);
+        }
       }
-      if constexpr (!std::is_void_v<W>) store4((W*)a.working + row + at_j, n, th[j]);
+      store4(theta + e, n, th[j]);
+      store_codes(m + e, n, (mcode & ~mbad) | (kNaNs & mbad));
+      store_codes(v + e, n, (vcode & ~vbad) | (kNaNs & vbad));
+      if (n > 0 && e % kCodeBlock == 0) {
+        ms[e / kCodeBlock] = (uint8_t)mbyte;
+        vs[e / kCodeBlock] = (uint8_t)vbyte;
+      }
+      if constexpr (!std::is_void_v<W>) store4((W*)a.working + row + e, n, th[j]);
     }
   };
-  if (s.count == 4 * kAdamWBlock * U) process(std::true_type());
-  else process(std::false_type());
+  // a block past a multiple of 2^32 elements has two sets of keys: the general path's case
+  if (full && !tiny_v_matters(r) && (uint32_t)s.base + kCodedTile > (uint32_t)s.base) finish(std::true_type());
+  else finish(std::false_type());
 }
 
 __global__ __launch_bounds__(64) void k_adamw_advance(const AdamWArgs a) {
@@ -574,11 +602,11 @@ __global__ __launch_bounds__(64) void k_adamw_advance(const AdamWArgs a) {
 
 template <typename G, typename W>
 hipError_t launch_adamw_gw(const AdamWArgs& a, bool coded, const InnerGeom& g, hipStream_t s) {
-  const dim3 grid(g.n_blocks, a.n_present), block(kAdamWBlock);
+  const dim3 grid(g.n_blocks, a.n_present);
   if (coded) {
-    hipLaunchKernelGGL((k_adamw_coded<G, W>), grid, block, 0, s, a, g);
+    hipLaunchKernelGGL((k_adamw_coded<G, W>), grid, dim3(kCodedBlock), 0, s, a, g);
   } else {
-    hipLaunchKernelGGL((k_adamw<G, W>), grid, block, 0, s, a, g);
+    hipLaunchKernelGGL((k_adamw<G, W>), grid, dim3(kAdamWBlock), kAdamWLds, s, a, g);
   }
   return hipGetLastError();
 }

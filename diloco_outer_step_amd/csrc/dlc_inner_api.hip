@@ -25,7 +25,7 @@ using dlc::round256;
 constexpr int64_t kNormBlocks = 2048;
 
 // A grid's x extent times its block must stay below 2^32 threads; a range has at most
-// 2^32 / 512 = 2^23 AdamW tiles.
+// 2^32 / 256 = 2^24 AdamW tiles of 64 threads.
 constexpr int64_t kMaxLaunchBlocks = int64_t(1) << 24;
 
 struct InnerPartition {
@@ -66,14 +66,27 @@ InnerPartition inner_partition(const std::vector<Range>& ranges, int64_t per_blo
         p.launches.back().n_blocks + blocks > kMaxLaunchBlocks) {
       p.launches.emplace_back();
       std::memset(&p.launches.back(), 0, sizeof(dlc::InnerGeom));
-      p.launches.back().per_block = per_block;
+      p.launches.back().per_block = (uint32_t)per_block;
       p.launches.back().slot_base = (int32_t)p.n_slots;
     }
     dlc::InnerGeom& g = p.launches.back();
-    g.r[g.n_ranges] = {(uint32_t)(r.lo / DLC_ALIGN_ELEMS), (uint32_t)r.count, (uint32_t)g.n_blocks};
-    g.group[g.n_ranges++] = (uint8_t)r.group;
+    g.r[g.n_ranges++] = {(uint32_t)(r.lo / DLC_ALIGN_ELEMS), (uint32_t)r.count,
+                         (uint32_t)g.n_blocks | (uint32_t)r.group << dlc::kGroupShift};
     g.n_blocks += (int32_t)blocks;
     p.n_slots += blocks;
+  }
+  for (dlc::InnerGeom& g : p.launches) {
+    while ((int64_t)(g.n_blocks - 1) >> g.bucket_shift >= dlc::kRangeBuckets) ++g.bucket_shift;
+    const auto range_of = [&](int64_t block, int32_t from) {
+      while (from + 1 < g.n_ranges && g.r[from + 1].block_first() <= block) ++from;
+      return from;
+    };
+    int32_t at = 0;
+    for (int64_t k = 0; k << g.bucket_shift < g.n_blocks; ++k) {
+      const int32_t first = range_of(k << g.bucket_shift, at);
+      at = range_of(std::min<int64_t>(g.n_blocks, (k + 1) << g.bucket_shift) - 1, first);
+      g.bucket[k] = (uint32_t)first | (uint32_t)at << 16;
+    }
   }
   return p;
 }
@@ -98,14 +111,14 @@ bool small_norm(const std::vector<Range>& ranges) {
 
 // Calls of at most this many blocks per learner count the step in the AdamW kernel itself:
 // one launch less is 2.7 us less where the host's launches are the time (11.4 against
-// 14.1 us for four vectors, 32 blocks), but tickets on one address pass at about 45 ns
-// each (9100 of them: 431 us for a call that takes 31).
-constexpr int64_t kMaxTickets = 32;
+// 14.1 us for four vectors), but tickets on one address pass at about 45 ns each (9100
+// of them: 431 us for a call that takes 31).
+constexpr int64_t kMaxTickets = 64;
 
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
-// The present learners' indices -> list, their number; 0 = an error was set.
-int32_t present_learners(int32_t n_learners, const uint8_t* present, uint8_t* list, int32_t* rc) {
+// The present learners' indices -> list (zeroed before), their number; *rc is the status.
+int32_t present_learners(int32_t n_learners, const uint8_t* present, dlc::LearnerList& list, int32_t* rc) {
   *rc = DLC_OK;
   if (n_learners < 1 || n_learners > DLC_MAX_LEARNERS) {
     *rc = fail(DLC_ERR_INVALID_ARGUMENT, "n_learners must be in [1, 64]");
@@ -113,7 +126,9 @@ int32_t present_learners(int32_t n_learners, const uint8_t* present, uint8_t* li
   }
   int32_t kp = 0;
   for (int32_t i = 0; i < n_learners; ++i) {
-    if (present == nullptr || present[i] != 0) list[kp++] = (uint8_t)i;
+    if (present != nullptr && present[i] == 0) continue;
+    list.word[kp >> 2] |= (uint32_t)i << (8 * (kp & 3));
+    ++kp;
   }
   if (kp == 0) *rc = fail(DLC_ERR_NO_QUORUM, "no learner is present");
   return kp;
@@ -199,7 +214,7 @@ int32_t adamw_step(float* theta_learners, const void* grads, int32_t grad_type, 
   a.seed = mo.seed;
   const hipStream_t s = static_cast<hipStream_t>(hip_stream);
   const InnerPartition p = inner_partition(join_tensors(tensors, n_tensors, group_of),
-                                           4 * dlc::kAdamWBlock * (mo.coded ? dlc::kCodedQuads : dlc::kAdamWQuads));
+                                           mo.coded ? dlc::kCodedTile : dlc::kAdamWTile);
   if (p.n_slots <= kMaxTickets && p.launches.size() == 1) a.tickets = (int32_t)p.n_slots;
   for (const dlc::InnerGeom& g : p.launches) {
     const hipError_t e = dlc::launch_adamw(a, grad_type, working ? working_type : dlc::kNone, mo.coded, g, s);

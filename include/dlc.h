@@ -518,8 +518,8 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
  *   grads       as dlc_grad_norm
  *   exp_avg     device fp32 [n_learners][learner_stride]: m (start with zeros)
  *   exp_avg_sq  device fp32 [n_learners][learner_stride]: v, never negative
- *   steps       device int64 [n_learners]: steps taken so far, counted up by the
- *               call.  It belongs to the call's tensors: a model stepped in several
+ *   steps       device int64 [n_learners]: steps taken so far (below 2^40), counted
+ *               up by the call.  It belongs to the call's tensors: a model stepped in several
  *               calls keeps one array for each.
  *   groups      host [n_groups], 1..DLC_MAX_GROUPS; lr and weight_decay finite and
  *               >= 0, betas in [0, 1), eps a normal positive fp32 number

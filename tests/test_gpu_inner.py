@@ -39,6 +39,10 @@ LISTS = {
     "joined": [64 * 7, 64, 4096, 64 * 70],                     # no padding: one range where the group is one
     "around_a_tile": [4095, 4096, 4097, 8191, 8192, 8193],
     "ragged": [1, 100003, 2, 65, 64 * 300 + 9, 4096 * 5 + 17, None, 31, 77777],
+    "few_blocks": [64 * 256],                                  # the most that a call's blocks count themselves ...
+    "more_blocks": [64 * 256 + 1],                             # ... and one more
+    "few_coded_blocks": [64 * 1024],
+    "more_coded_blocks": [64 * 1024 - 5, 6],
     "many": [(7 * i) % 200 + 1 for i in range(600)],           # more ranges than one launch takes
 }
 
