@@ -27,8 +27,11 @@ constexpr int kCodeBlock = 64;       // elements that share a scale byte
 constexpr int kAdamWBlock = 64;
 constexpr int kAdamWTile = 4 * kAdamWBlock;
 constexpr int kAdamWLds = 14800;
-// With coded moments: two waves, eight elements a thread (twice the arithmetic per byte, and
-// loads of 4 bytes: one quad a thread was 8% slower); its registers already leave 20 waves a CU.
+// With coded moments: two waves, two quads a thread 256 elements apart.  Twice the
+// arithmetic per byte and code loads of 4 bytes a lane: one quad a thread took 3.20 ms against 2.95
+// on eight 135M learners; eight consecutive elements a thread, whose fp32 accesses are no
+// longer whole kilobytes a wave, 3.48 against 2.86.  Its registers leave 20 waves a CU; fewer are
+// slower.
 constexpr int kCodedBlock = 128;
 constexpr int kCodedQuads = 2;
 constexpr int kCodedTile = 4 * kCodedBlock * kCodedQuads;

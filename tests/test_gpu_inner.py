@@ -162,6 +162,22 @@ def test_adamw_64_learners():
     check_adamw([100, 4097], GROUPS[:2], lambda j: j, "fp32", "", [int(i % 5 != 0) for i in range(64)], k=64)
 
 
+def test_adamw_tiny_second_moments_under_a_tiny_eps():
+    """v among the subnormals, where its root still outweighs eps: neither is lost."""
+    def change(b, tensors):
+        for _, lo, n in tensors:
+            b["v"][:, lo:lo + n].mul_(1e-36), b["m"][:, lo:lo + n].mul_(1e-18), b["grads"][:, lo:lo + n].mul_(1e-18)
+
+    for eps in (1.2e-38, 1e-25, 1e-21, 1e-18, 1e-11):
+        groups = [dlc.AdamWGroup(1e-3, 0.9, 0.999, eps, 0.1), dlc.AdamWGroup(1e-3, 0.9, 0.5, eps, 0.0)]
+        for start in (0, 500):
+            def both(b, tensors):
+                change(b, tensors)
+                b["steps"].fill_(start)
+
+            check_adamw([1, 65, 4099, 256], groups, lambda j: j % 2, "fp32", "", [1, 1], k=2, change=both)
+
+
 @pytest.mark.parametrize("scale", [0.0, -1.0, math.inf, -math.inf, math.nan])
 def test_a_learner_without_a_usable_scale_is_left_out(scale):
     check_adamw(LISTS["ragged"], GROUPS, lambda j: j % 3, "fp32", "bf16", [1, 1, 1], clip=[1.0, scale, 0.25])
@@ -286,6 +302,17 @@ def coded_call(b, tensors, groups, ids, seed, clip, lr_scale, work, present, str
 
 
 CODED = ("theta", "mc", "ms", "vc", "vs", "steps")
+
+
+def test_coded_tiny_moments_under_a_tiny_eps():
+    def change(b, tensors):
+        for n in ("mc", "ms", "vc", "vs"):
+            b[n].zero_()
+        b["grads"].mul_(1e-16)
+
+    for eps in (1.2e-38, 1e-24, 1e-19):
+        check_coded([1, 65, 4099, 1024], [dlc.AdamWGroup(1e-3, 0.9, 0.999, eps, 0.1)], None, "fp32", "", [1, 1], k=2,
+                    change=change, times=3)
 
 
 def check_coded(case, groups, group_of, grads, working, present, clip=None, lr_scale=None, shuffle=0, k=3, seed=9,
@@ -458,12 +485,13 @@ class Far:
             inner.random_words = words
 
 
+@pytest.mark.parametrize("name", ["ragged", "around_a_block"])  # the step counted by a kernel of its own, by the blocks
 @pytest.mark.parametrize("coded", [False, True])
-def test_captured_steps_replay_the_eager_ones(coded):
+def test_captured_steps_replay_the_eager_ones(coded, name):
     """Norm and step captured once: every replay counts its own step, reads the schedule's
-    factor and the gradients of the moment, and equals the eager calls; two graphs of two
-    tensor lists share nothing but the gradients."""
-    tensors, stride = layout(LISTS["ragged"])
+    factor and the gradients of the moment, and equals the eager calls; two graphs with
+    buffers of their own run one after the other."""
+    tensors, stride = layout(LISTS[name])
     plan = dlc.TensorList(tensors)
     k = 3
 

@@ -191,6 +191,43 @@ def test_a_tensor_list_is_the_list_it_was_made_from():
     assert dlc.group_ids([0, 1]).dtype == np.int32
 
 
+def test_a_call_runs_on_its_buffers_device_and_stream(monkeypatch):
+    """Buffers on another device than the current one: that device is current during the call and its
+    own current stream is used; a stream of another device is refused."""
+    seen = []
+
+    class Guard:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            seen.append(("enter", self.index))
+
+        def __exit__(self, *exc):
+            seen.append(("exit", self.index))
+
+    class Stream:
+        def __init__(self, index):
+            self.device, self.cuda_stream = torch.device("cuda", index), 777
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index, raising=False)
+
+    def fn(*args):
+        seen.append(args)
+        return 0
+
+    dlc._on_device(0, None, fn, 5)
+    dlc._on_device(1, None, fn, 6)
+    assert seen == [(5, 1000), ("enter", 1), (6, 1001), ("exit", 1)]
+    dlc._on_device(1, Stream(1), fn, 7)
+    assert seen[-2][1].value == 777
+    with pytest.raises(ValueError, match="stream is on cuda:0"):
+        dlc._on_device(1, Stream(0), fn, 8)
+
+
 @pytest.mark.skipif(not os.path.exists(CLANG) or asan_runtime() is None,
                     reason="ROCm clang with the sanitizer runtimes is not installed")
 @pytest.mark.skipif("DLC_LIBRARY" in os.environ, reason="already under the sanitizers")
