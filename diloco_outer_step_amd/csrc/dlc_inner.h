@@ -40,7 +40,7 @@ constexpr int kCodedTile = 4 * kCodedBlock * kCodedQuads;
 // 16384 blocks are within 4%; steps dealt out in turn are 2% slower).
 constexpr int kNormBlock = 256;
 constexpr int kNormLoads = 4;
-constexpr int kNormStep = kNormBlock * kNormLoads * 4;  // elements, fp32
+constexpr int kNormStep = kNormBlock * kNormLoads * 16;  // bytes
 constexpr int kNormFinal = 1024;     // threads of the final sum
 
 enum FloatType : int32_t { kF32 = 0, kBF16 = 1, kF16 = 2, kNone = -1 };

@@ -29,7 +29,6 @@ namespace dlc {
 namespace {
 
 typedef float vf4 __attribute__((ext_vector_type(4)));
-typedef unsigned int vu2 __attribute__((ext_vector_type(2)));
 
 // Block -> (group, first element of the row, elements).  The launch geometry lives in the
 // kernel arguments and is read by scalar loads; the bucket of the block number leaves few
@@ -66,19 +65,6 @@ __device__ __forceinline__ void load4(const float* p, int n, float (&x)[4]) {
   } else {
 #pragma unroll
     for (int c = 0; c < 4; ++c) x[c] = c < n ? p[c] : 0.0f;
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, int n, float (&x)[4]) {
-  typedef T v4 __attribute__((ext_vector_type(4)));
-  if (n >= 4) {
-    const v4 q = __builtin_nontemporal_load((const v4*)p);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = (float)q[c];
-  } else {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = c < n ? (float)p[c] : 0.0f;
   }
 }
 

@@ -97,9 +97,10 @@ int64_t total_elements(const std::vector<Range>& ranges) {
   return n;
 }
 
-InnerPartition norm_partition(const std::vector<Range>& ranges) {
-  const int64_t steps = (total_elements(ranges) + dlc::kNormStep - 1) / dlc::kNormStep;
-  return inner_partition(ranges, dlc::kNormStep * std::max<int64_t>(1, (steps + kNormBlocks - 1) / kNormBlocks));
+InnerPartition norm_partition(const std::vector<Range>& ranges, int32_t bytes_per_element) {
+  const int64_t step = dlc::kNormStep / bytes_per_element;
+  const int64_t steps = (total_elements(ranges) + step - 1) / step;
+  return inner_partition(ranges, step * std::max<int64_t>(1, (steps + kNormBlocks - 1) / kNormBlocks));
 }
 
 // Few elements in few ranges: one block per learner does it all.
@@ -239,7 +240,8 @@ int32_t dlc_grad_norm_workspace_bytes(int32_t n_learners, const dlc_tensor* tens
       return fail(DLC_ERR_INVALID_ARGUMENT, "n_learners must be in [1, 64]");
     const int32_t rc = check_tensors(tensors, n_tensors, 0, false);
     if (rc != DLC_OK) return rc;
-    const InnerPartition p = norm_partition(join_tensors(tensors, n_tensors, nullptr));
+    // blocks of 16-bit gradients have at least as many elements: no type has more slots than fp32
+    const InnerPartition p = norm_partition(join_tensors(tensors, n_tensors, nullptr), 4);
     *bytes = round256((size_t)p.n_slots * n_learners * sizeof(double));
     return ok();
   });
@@ -268,7 +270,7 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
       return fail(DLC_ERR_INVALID_ARGUMENT, "unscale must be finite and > 0");
     if (!(max_norm > 0.0)) return fail(DLC_ERR_INVALID_ARGUMENT, "max_norm must be > 0");
     const std::vector<Range> ranges = join_tensors(tensors, n_tensors, nullptr);
-    const InnerPartition p = norm_partition(ranges);
+    const InnerPartition p = norm_partition(ranges, grad_type == DLC_FLOAT32 ? 4 : 2);
     const size_t need = round256((size_t)p.n_slots * a.n_present * sizeof(double));
     if (workspace == nullptr || workspace_bytes < need)
       return fail(DLC_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");

@@ -491,7 +491,8 @@ int32_t dlc_rda_outer_step(float* theta_global, float* momentum, const float* th
  *   norm, grad_scale  device fp64 [n_learners], written for present learners
  *   workspace   >= dlc_grad_norm_workspace_bytes(n_learners, tensors, n_tensors)
  *               bytes, 256-byte aligned, no initial contents required
- * The sum's order depends on the tensor list alone: repeated calls agree bit for bit.
+ * The sum's order depends on the tensor list and grad_type alone: repeated calls agree
+ * bit for bit.
  */
 int32_t dlc_grad_norm_workspace_bytes(int32_t n_learners, const dlc_tensor* tensors, int32_t n_tensors,
                                       size_t* bytes);

@@ -469,18 +469,65 @@ def test_elements_beyond_2_to_the_32(coded):
     same(np.where(s["mask"], 0, host(big["theta"][:, lo:])), np.where(s["mask"], 0, start), "theta's sentinels")
 
 
+@pytest.mark.parametrize("coded", [False, True])
+def test_the_largest_tensor(coded):
+    """2^32 - 1 elements and a short tensor behind them, in two launches: windows at the start, around the middle
+    and at the end against the oracle, every element against a fill that the step cannot leave."""
+    big = (1 << 32) - 1
+    tensors = [(0, 0, big), (1 << 32, 1 << 32, 5000)]
+    stride = (1 << 32) + 8192
+    windows = [(0, 4096), ((1 << 31) - 2048, 4096), (big - 4095, 4095), (1 << 32, 5000)]
+    gen = torch.Generator().manual_seed(1)
+    theta = torch.full((1, stride), 1.0, device=DEV)
+    grads = torch.full((1, stride), 0.25, dtype=torch.bfloat16, device=DEV)
+    for lo, n in windows:
+        theta[0, lo:lo + n] = (torch.randn(n, generator=gen) * 0.02).to(DEV)
+        grads[0, lo:lo + n] = torch.randn(n, generator=gen).to(torch.bfloat16).to(DEV)
+    steps = torch.zeros(1, dtype=torch.int64, device=DEV)
+    start = [host(theta[:, lo:lo + n]).copy() for lo, n in windows]
+    gr = [host(grads[:, lo:lo + n]) for lo, n in windows]
+    if coded:
+        mc, ms, vc, vs = dlc.coded_moments(1, stride)
+        dlc.dlc_adamw_coded_step(theta, grads, mc, ms, vc, vs, steps, tensors, GROUPS[0], seed=2)
+    else:
+        m, v = torch.zeros_like(theta), torch.zeros_like(theta)
+        dlc.dlc_adamw_step(theta, grads, m, v, steps, tensors, GROUPS[0])
+    torch.cuda.synchronize()
+    assert int(steps[0]) == 1
+    assert bool((theta[0, big + 1 + 5000:] == 1.0).all())
+    for at in range(0, big, 1 << 28):
+        assert not bool((theta[0, at:min(big, at + (1 << 28))] == 1.0).any()), at
+    for (lo, n), th, g in zip(windows, start, gr):
+        zero = [np.zeros((1, n), np.float32) for _ in range(2)]
+        count = np.zeros(1, np.int64)
+        if coded:
+            blocks = -(-n // 64)
+            r = dict(theta=th, mc=np.zeros((1, n), np.uint8), ms=np.zeros((1, blocks), np.uint8),
+                     vc=np.zeros((1, n), np.uint8), vs=np.zeros((1, blocks), np.uint8), steps=count)
+            whole = n if lo + n != big else n - n % 64  # a window that ends inside a block: its whole blocks
+            size = Far(r, lo).step(g, [(0, 0, n)], None, seed=2)
+            same(host(mc.view(torch.uint8)[:, lo:lo + n]), r["mc"], "m")
+            same(host(vc.view(torch.uint8)[:, lo:lo + n]), r["vc"], "v")
+            same(host(ms[:, lo // 64:(lo + whole) // 64]), r["ms"][:, :whole // 64], "m scales")
+        else:
+            size = inner.adamw(th, g, zero[0], zero[1], count, [(0, 0, n)], GROUPS)
+            same(host(m[:, lo:lo + n]), zero[0], "m")
+            same(host(v[:, lo:lo + n]), zero[1], "v")
+        near_theta(host(theta[:, lo:lo + n]), th, size, np.ones((1, n), bool), "theta")
+
+
 class Far:
     """The oracle's coded step on a short row whose element 0 is element `lo` of the real one."""
 
     def __init__(self, ref, lo):
         self.ref, self.lo = ref, lo
 
-    def step(self, grads, tensors, clip):
+    def step(self, grads, tensors, clip, seed=4):
         words, r = inner.random_words, self.ref
         inner.random_words = lambda seed, t, i, lo, n: words(seed, t, i, lo + self.lo, n)
         try:
             return inner.adamw_coded(r["theta"], grads, r["mc"], r["ms"], r["vc"], r["vs"], r["steps"], tensors, GROUPS,
-                                     None, 4, clip)
+                                     None, seed, clip)
         finally:
             inner.random_words = words
 
