@@ -606,6 +606,43 @@ def test_calls_on_another_stream_follow_that_stream():
         assert torch.equal(a[n], b[n])
 
 
+def test_two_streams_at_once_with_buffers_of_their_own():
+    """Norm and step of two models, four passes each, side by side on two streams: as one after the other."""
+    tensors, stride = layout([1 << 21, 12345, 64 * 1000])
+    plan = dlc.TensorList(tensors)
+
+    def state(seed):
+        b = draw(2, stride, tensors, [1, 1], "bf16", seed)
+        coded_start(b, 2, stride, seed)
+        b["norm"], b["scale"] = (torch.zeros(2, dtype=torch.float64, device=DEV) for _ in range(2))
+        b["ws"] = dlc.alloc_grad_norm_workspace(2, plan)
+        return b
+
+    def steps(b, coded, stream):
+        for _ in range(4):
+            dlc.dlc_grad_norm(b["grads"], plan, b["norm"], b["scale"], b["ws"], max_norm=0.5, stream=stream)
+            if coded:
+                dlc.dlc_adamw_coded_step(b["theta"], b["grads"], b["mc"].view(torch.float8_e4m3fn), b["ms"],
+                                         b["vc"].view(torch.float8_e5m2), b["vs"], b["steps"], plan, seed=3,
+                                         grad_scale=b["scale"], stream=stream)
+            else:
+                dlc.dlc_adamw_step(b["theta"], b["grads"], b["m"], b["v"], b["steps"], plan, grad_scale=b["scale"],
+                                   stream=stream)
+
+    alone, beside = [state(1), state(2)], [state(1), state(2)]
+    for k, b in enumerate(alone):
+        steps(b, k == 1, None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for k, b in enumerate(beside):
+        steps(b, k == 1, streams[k])
+    torch.cuda.synchronize()
+    for a, b in zip(alone, beside):
+        for n in a:
+            if n not in ("mask", "ws"):
+                assert torch.equal(a[n], b[n]), n
+
+
 @pytest.mark.parametrize("coded", [False, True])
 def test_two_whole_rounds_of_inner_and_outer_steps(coded):
     """What the calls are for: H inner steps of every learner (norm, clipping, AdamW), then the
