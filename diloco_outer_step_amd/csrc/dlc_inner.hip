@@ -56,16 +56,14 @@ __device__ __forceinline__ Spot spot(const InnerGeom& g, uint32_t per_block) {
   return s;
 }
 
-// Four elements at p, the first n of them valid (n may be <= 0 or >= 4); others read as 0.
+// Loads of four elements at p, the first n of them the tensor's (n may be <= 0 or >= 4).
+// Tensors start, and rows end, at multiples of 64 elements, so the four lie within the row
+// if the first does: they are loaded whole, and what is behind the tensor is not used.
 __device__ __forceinline__ void load4(const float* p, int n, float (&x)[4]) {
-  if (n >= 4) {
-    const vf4 q = __builtin_nontemporal_load((const vf4*)p);
+  vf4 q = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (n > 0) q = __builtin_nontemporal_load((const vf4*)p);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = q[c];
-  } else {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = c < n ? p[c] : 0.0f;
-  }
+  for (int c = 0; c < 4; ++c) x[c] = q[c];
 }
 
 template <typename T>
@@ -84,18 +82,14 @@ __device__ __forceinline__ void store4(T* p, int n, const float (&x)[4]) {
   }
 }
 
-// Four gradients as they lie in memory, the first n of them valid.
+// Four gradients as they lie in memory.
 template <typename G>
 struct Raw4 {
   typedef G v4 __attribute__((ext_vector_type(4)));
   v4 q;
   __device__ __forceinline__ void load(const G* p, int n) {
-    if (n >= 4) {
-      q = __builtin_nontemporal_load((const v4*)p);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) q[c] = c < n ? p[c] : (G)0.0f;
-    }
+    q = v4{};
+    if (n > 0) q = __builtin_nontemporal_load((const v4*)p);
   }
   __device__ __forceinline__ float value(int c) const { return (float)q[c]; }
 };
@@ -153,13 +147,9 @@ __device__ __forceinline__ double squares(const G* p, int64_t count) {
     for (int j = 0; j < U; ++j) add(y[j]);
   }
   for (int64_t e = at + (int64_t)V * threadIdx.x; e < count; e += (int64_t)V * kThreads) {
-    vec x;
-    if (count - e >= V) {
-      x = __builtin_nontemporal_load((const vec*)(p + e));
-    } else {
+    vec x = __builtin_nontemporal_load((const vec*)(p + e));  // within the row, see load4
 #pragma unroll
-      for (int c = 0; c < V; ++c) x[c] = c < count - e ? p[e + c] : (G)0.0f;
-    }
+    for (int c = 0; c < V; ++c) x[c] = c < count - e ? x[c] : (G)0.0f;
     add(x);
   }
   return (s[0] + s[1]) + (s[2] + s[3]);
@@ -432,13 +422,7 @@ __device__ __forceinline__ void decode_v(uint32_t w, float (&x)[4]) {
 }
 
 __device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int n) {
-  if (n >= 4) return __builtin_nontemporal_load((const uint32_t*)p);
-  uint32_t w = 0;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (c < n) w |= (uint32_t)p[c] << (8 * c);
-  }
-  return w;
+  return n > 0 ? __builtin_nontemporal_load((const uint32_t*)p) : 0u;
 }
 
 __device__ __forceinline__ void store_codes(uint8_t* p, int n, uint32_t w) {

@@ -469,10 +469,12 @@ int32_t dlc_rda_outer_step(float* theta_global, float* momentum, const float* th
  * norm with its clipping factor, then AdamW with 32-bit or with 8-bit moments.
  * Gradients and moments are laid out like the learner rows ([n_learners] rows of
  * learner_stride elements, tensor t at [loffset, loffset + numel); a tensor's
- * `offset` is not used, though the list has to satisfy the rules above).  Only elements of the call's tensors in present learners'
- * rows are read or written.  Nothing synchronizes, nothing is kept between calls
- * but the caller's buffers, and results do not depend on how the tensors are
- * ordered or split over launches: a call can be captured in a HIP graph and replayed.
+ * `offset` is not used, though the list has to satisfy the rules above).  Only
+ * elements of the call's tensors in present learners' rows are written, and nothing
+ * else has any influence (a tensor's last group of 64 elements may be read whole).
+ * Nothing synchronizes, nothing is kept between calls but the caller's buffers, and
+ * AdamW's results do not depend on how the tensors are ordered or split over calls: a
+ * call can be captured in a HIP graph and replayed.
  */
 
 /*
