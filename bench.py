@@ -73,7 +73,7 @@ def parse():
                          "and print them as one JSON line")
     ap.add_argument("--reported-only", default=None,
                     help="comma-separated subset of c1,c4_largest,c2,c5k1,c5k16,native_c2,native_c5k1,"
-                         "broadcast_c3,stale_c3,ring_study,ring_c3,rda_c3")
+                         "broadcast_c3,stale_c3,ring_study,ring_c3,rda_c3,inner_c3")
     ap.add_argument("--copy-probe", action="store_true",
                     help="only run a device-to-device copy of known size (counter calibration)")
     return ap.parse_args()
@@ -595,14 +595,63 @@ def rda_rate(key, device, reps=5, warmup=2):
                 hbm_gbps=b / (ms_ * 1e-3) / 1e9, hbm_frac=b / (ms_ * 1e-3) / 8e12, bytes_per_param=24 + 11 * kp)
 
 
+def inner_rate(key, device, reps=10, warmup=3):
+    """One inner step of every learner of a set, bf16 gradients and working copy: the norm
+    (2 bytes per element), AdamW with 32-bit moments (28) and with coded moments (16 + 4/64)."""
+    import statistics
+    import torch
+    import diloco_outer_step_amd as dlc
+    import workloads
+    cfg = workloads.config(key)
+    inp = workloads.fragment_inputs(cfg, list(range(len(cfg.tensors))), device)
+    k, stride = inp.theta_L.shape
+    plan = dlc.TensorList(inp.tensors)
+    ids = dlc.group_ids([1 if s.kind == "norm" else 0 for s in cfg.tensors])
+    groups = [dlc.AdamWGroup(1e-4, 0.9, 0.95, 1e-8, wd) for wd in (0.1, 0.0)]
+    gen = torch.Generator(device).manual_seed(0)
+    grads = torch.empty((k, stride), dtype=torch.bfloat16, device=device).normal_(generator=gen).mul_(1e-3)
+    work = inp.theta_L.to(torch.bfloat16)
+    m, v = torch.zeros_like(inp.theta_L), torch.zeros_like(inp.theta_L)
+    coded = dlc.coded_moments(k, stride, device)
+    steps = [torch.zeros(k, dtype=torch.int64, device=device) for _ in range(2)]
+    norm, scale = (torch.zeros(k, dtype=torch.float64, device=device) for _ in range(2))
+    ws = dlc.alloc_grad_norm_workspace(k, plan, device)
+    common = dict(group_of=ids, grad_scale=scale, working=work)
+    calls = {
+        "grad_norm": (2, lambda: dlc.dlc_grad_norm(grads, plan, norm, scale, ws, max_norm=1.0)),
+        "adamw": (28, lambda: dlc.dlc_adamw_step(inp.theta_L, grads, m, v, steps[0], plan, groups, **common)),
+        "adamw_coded": (16 + 4 / dlc.DLC_CODE_BLOCK, lambda: dlc.dlc_adamw_coded_step(
+            inp.theta_L, grads, *coded, steps[1], plan, groups, seed=1, **common)),
+    }
+    n = sum(x for _, _, x in inp.tensors) * k
+    out = dict(workload=cfg.title, elements=n, learners=k)
+    for name, (per, run) in calls.items():
+        for _ in range(warmup):
+            run()
+        torch.cuda.synchronize()
+        ts = []
+        for _ in range(reps):
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            e0.record()
+            run()
+            e1.record()
+            torch.cuda.synchronize()
+            ts.append(e0.elapsed_time(e1))
+        ms_ = statistics.median(ts)
+        out[name] = dict(ms=ms_, bytes_per_element=per, hbm_gbps=per * n / (ms_ * 1e-3) / 1e9,
+                         hbm_frac=per * n / (ms_ * 1e-3) / 1e9 / PEAK_HBM_GBPS)
+    return out
+
+
 def reported(device, only=None):
     """The parameter sets that are reported but not gated: the 4096^2 tensor (cold
     cache), the 10B set's largest fragment, full 24-fragment cycles of the 135M set
-    and of the edge mix, and the calls of the next rows on the 1B set."""
+    and of the edge mix, the calls of the next rows on the 1B set, and the learners'
+    inner step on it."""
     import torch
     keys = only.split(",") if only else ["c1", "c4_largest", "c2", "c5k1", "c5k16", "native_c2", "native_c5k1",
                                          "broadcast_c3",
-                                         "stale_c3", "ring_study", "ring_c3", "rda_c3"]
+                                         "stale_c3", "ring_study", "ring_c3", "rda_c3", "inner_c3"]
     out = {}
     if "c1" in keys:
         out["c1"] = single_call_cold("c1", device)
@@ -627,6 +676,11 @@ def reported(device, only=None):
         out["rda_c3"] = rda_rate("c3", device)
         torch.cuda.empty_cache()
         print(f"# rda c3 {out['rda_c3']['ms']:.3f} ms", file=sys.stderr, flush=True)
+    if "inner_c3" in keys:
+        out["inner_c3"] = inner_rate("c3", device)
+        torch.cuda.empty_cache()
+        print("# inner step c3: " + ", ".join(f"{n} {v['ms']:.3f} ms" for n, v in out["inner_c3"].items()
+                                              if isinstance(v, dict)), file=sys.stderr, flush=True)
     if "ring_study" in keys:
         out["ring_study"] = ring_study(device)
         torch.cuda.empty_cache()

@@ -515,8 +515,8 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
  *   working <- theta rounded to working_type (nearest even)
  *   steps[i] <- t
  * m and v are computed in fp64 and rounded to fp32 once; the change of theta is an
- * fp32 expression of the rounded moments, within 2^-20 of its value, and is
- * subtracted with one rounding.
+ * fp32 expression of the rounded moments, within 2^-20 of its two terms' magnitudes,
+ * and is subtracted with one rounding.
  *   theta_learners  device fp32 [n_learners][learner_stride], updated in place
  *   grads       as dlc_grad_norm
  *   exp_avg     device fp32 [n_learners][learner_stride]: m (start with zeros)
