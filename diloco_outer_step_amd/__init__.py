@@ -11,6 +11,7 @@ Importing this package fails loudly if the library has not been built
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import itertools
 import os
@@ -80,10 +81,6 @@ class AdamWGroup(NamedTuple):
     weight_decay: float = 0.01
 
 
-class _Group(ctypes.Structure):
-    _fields_ = [(name, ctypes.c_double) for name in AdamWGroup._fields]
-
-
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python diloco_outer_step_amd/build.py`")
@@ -118,9 +115,9 @@ def _load() -> ctypes.CDLL:
                                 ctypes.c_double, u32, vp, sz, vp, i32],
         "dlc_grad_norm_workspace_bytes": [i32, tp, i32, ctypes.POINTER(sz)],
         "dlc_grad_norm": [vp, i32, i64, i32, vp, tp, i32, ctypes.c_double, ctypes.c_double, vp, vp, vp, sz, vp],
-        "dlc_adamw_step": [vp, vp, i32, vp, vp, vp, i64, i32, vp, tp, i32, vp, ctypes.POINTER(_Group), i32, vp, vp,
+        "dlc_adamw_step": [vp, vp, i32, vp, vp, vp, i64, i32, vp, tp, i32, vp, vp, i32, vp, vp,
                            vp, i32, vp],
-        "dlc_adamw_coded_step": [vp, vp, i32, vp, vp, vp, vp, vp, i64, i32, vp, tp, i32, vp, ctypes.POINTER(_Group),
+        "dlc_adamw_coded_step": [vp, vp, i32, vp, vp, vp, vp, vp, i64, i32, vp, tp, i32, vp, vp,
                                  i32, ctypes.c_uint64, vp, vp, vp, i32, vp],
     }
     for name, args in sig.items():
@@ -700,9 +697,11 @@ def _address(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def group_ids(group_of: Sequence[int]) -> np.ndarray:
+def group_ids(group_of: Sequence[int]) -> array.array:
     """Group of each tensor as the C ABI reads it (a training loop converts it once)."""
-    return np.ascontiguousarray(group_of, dtype=np.int32)
+    if isinstance(group_of, array.array) and group_of.typecode == "i":
+        return group_of
+    return array.array("i", [int(g) for g in group_of])
 
 
 def dlc_grad_norm_workspace_bytes(n_learners: int, tensors) -> int:
@@ -767,20 +766,23 @@ def _adamw(theta_L, grads, moments, steps, tensors, groups, group_of, grad_scale
         bufs.append(("working", working, working.dtype, rows))
     if isinstance(groups, AdamWGroup):
         groups = (groups,)
-    gs = (_Group * max(1, len(groups)))(*groups)
+    gs = array.array("d", itertools.chain.from_iterable(groups))
+    if len(gs) != len(AdamWGroup._fields) * len(groups):
+        raise ValueError("groups must hold AdamWGroup entries")
     ids = None
     if group_of is not None:
         ids = group_ids(group_of)
-        if ids.shape != (len(tensors),):
-            raise ValueError(f"group_of holds {ids.size} values for {len(tensors)} tensors")
+        if len(ids) != len(tensors):
+            raise ValueError(f"group_of holds {len(ids)} values for {len(tensors)} tensors")
     _check_buffers(bufs)
     arr, n = _tensors(tensors)
     return (gt, stride, k, pres, arr, n, ids, gs, len(groups), _address(grad_scale), _address(lr_scale),
             _address(working), wt)
 
 
-def _ids_address(ids) -> Optional[int]:
-    return None if ids is None else ids.__array_interface__["data"][0]
+def _items(a: Optional[array.array]) -> Optional[int]:
+    """Address of an array's items (the array is kept by the caller during the call)."""
+    return None if a is None else a.buffer_info()[0]
 
 
 def dlc_adamw_step(theta_L, grads, exp_avg, exp_avg_sq, steps, tensors, groups=AdamWGroup(), group_of=None,
@@ -795,8 +797,8 @@ def dlc_adamw_step(theta_L, grads, exp_avg, exp_avg_sq, steps, tensors, groups=A
         theta_L, grads, (("exp_avg", exp_avg, torch.float32, 1), ("exp_avg_sq", exp_avg_sq, torch.float32, 1)), steps,
         tensors, groups, group_of, grad_scale, lr_scale, working, present)
     _on_device(theta_L.get_device(), stream, _lib.dlc_adamw_step, theta_L.data_ptr(), grads.data_ptr(), gt,
-               exp_avg.data_ptr(), exp_avg_sq.data_ptr(), steps.data_ptr(), stride, k, pres, arr, n, _ids_address(ids),
-               gs, ng, scale, lrs, work, wt)
+               exp_avg.data_ptr(), exp_avg_sq.data_ptr(), steps.data_ptr(), stride, k, pres, arr, n, _items(ids),
+               _items(gs), ng, scale, lrs, work, wt)
 
 
 def dlc_adamw_coded_step(theta_L, grads, m_codes, m_scales, v_codes, v_scales, steps, tensors, groups=AdamWGroup(),
@@ -814,4 +816,4 @@ def dlc_adamw_coded_step(theta_L, grads, m_codes, m_scales, v_codes, v_scales, s
         steps, tensors, groups, group_of, grad_scale, lr_scale, working, present)
     _on_device(theta_L.get_device(), stream, _lib.dlc_adamw_coded_step, theta_L.data_ptr(), grads.data_ptr(), gt,
                m_codes.data_ptr(), m_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), steps.data_ptr(),
-               stride, k, pres, arr, n, _ids_address(ids), gs, ng, int(seed), scale, lrs, work, wt)
+               stride, k, pres, arr, n, _items(ids), _items(gs), ng, int(seed), scale, lrs, work, wt)

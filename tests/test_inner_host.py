@@ -40,7 +40,8 @@ def norm(k=2, spec=((0, 0, 4096),), stride=4096, grads=F[0], gt=0, present=None,
 def step(coded, k=2, spec=((0, 0, 4096),), stride=4096, theta=F[0], grads=F[1], gt=0, m=F[2], v=F[3], ms=F[4], vs=F[5],
          steps=F[6], present=None, groups=(GOOD,), n_groups=None, group_of=None, gs=None, lrs=None, work=None, wt=1):
     arr, n = tens(spec)
-    g = None if groups is None else (dlc._Group * max(1, len(groups)))(*groups)
+    flat = [x for g in groups or () for x in g]
+    g = None if groups is None else ctypes.cast((ctypes.c_double * max(1, len(flat)))(*flat), ctypes.c_void_p)
     ids = None if group_of is None else ctypes.cast((ctypes.c_int32 * len(group_of))(*group_of), ctypes.c_void_p)
     ng = (0 if groups is None else len(groups)) if n_groups is None else n_groups
     if coded:
@@ -174,6 +175,8 @@ def test_lists_must_match_the_call(name):
     if name != "norm":
         with pytest.raises(ValueError, match="group_of holds 3 values for 2 tensors"):
             call(name, good(), group_of=[0, 0, 0])
+        with pytest.raises(ValueError, match="AdamWGroup"):
+            call(name, good(), groups=[(1e-3, 0.9)])
     if name == "coded":
         for seed in (-1, 1 << 64):
             with pytest.raises(ValueError, match="seed"):
@@ -188,7 +191,8 @@ def test_a_tensor_list_is_the_list_it_was_made_from():
     arr, n = dlc._tensors(t)
     assert n == 2 and (arr[1].offset, arr[1].loffset, arr[1].numel) == TENSORS[1]
     assert dlc._tensors(dlc.TensorList([]))[1] == 0
-    assert dlc.group_ids([0, 1]).dtype == np.int32
+    ids = dlc.group_ids(np.array([0, 1]))
+    assert list(ids) == [0, 1] and ids.itemsize == 4 and dlc.group_ids(ids) is ids
 
 
 def test_a_call_runs_on_its_buffers_device_and_stream(monkeypatch):
