@@ -135,10 +135,68 @@ int32_t present_learners(int32_t n_learners, const uint8_t* present, dlc::Learne
   return kp;
 }
 
+// What a call uses of one of its device arrays: for learner i, `bytes` bytes at base + i * pitch
+// (addresses as numbers; an absent array has no bytes).
+struct Use {
+  uintptr_t base;
+  uint64_t pitch, bytes;
+  bool written;
+};
+
+// A row buffer's elements of `size` bytes, from the first tensor's start to the last one's end.
+struct RowSpan {
+  int64_t first, last;
+  RowSpan(const dlc_tensor* t, int32_t n) : first(t[0].loffset), last(0) {
+    for (int32_t i = 0; i < n; ++i) {
+      first = std::min(first, t[i].loffset);
+      last = std::max(last, t[i].loffset + t[i].numel);
+    }
+  }
+  Use rows(const void* p, int64_t stride, int64_t size, bool written) const {
+    return {reinterpret_cast<uintptr_t>(p) + uint64_t(first) * size, uint64_t(stride) * size,
+            p ? uint64_t(last - first) * size : 0, written};
+  }
+  Use scales(const void* p, int64_t stride) const {
+    const int64_t lo = first / DLC_CODE_BLOCK, hi = (last + DLC_CODE_BLOCK - 1) / DLC_CODE_BLOCK;
+    return {reinterpret_cast<uintptr_t>(p) + uint64_t(lo), uint64_t(stride) / DLC_CODE_BLOCK, p ? uint64_t(hi - lo) : 0,
+            true};
+  }
+};
+
+Use per_learner(const void* p, bool written) {
+  return {reinterpret_cast<uintptr_t>(p), sizeof(double), p ? sizeof(double) : 0, written};
+}
+
+bool apart(const Use& a, const Use& b, const dlc::LearnerList& learner, int32_t n) {
+  const auto clear = [](uintptr_t x, uint64_t nx, uintptr_t y, uint64_t ny) { return x + nx <= y || y + ny <= x; };
+  if (a.bytes == 0 || b.bytes == 0) return true;
+  const uint64_t lo = learner[0], span = learner[n - 1] - lo;
+  if (clear(a.base + lo * a.pitch, span * a.pitch + a.bytes, b.base + lo * b.pitch, span * b.pitch + b.bytes)) return true;
+  for (int32_t i = 0; i < n; ++i) {  // rows of two buffers may still take turns
+    for (int32_t j = 0; j < n; ++j) {
+      if (!clear(a.base + learner[i] * a.pitch, a.bytes, b.base + learner[j] * b.pitch, b.bytes)) return false;
+    }
+  }
+  return true;
+}
+
+// No array that is written may share memory with another one: blocks of a launch run in any order.
+int32_t check_apart(const Use* use, int32_t n_uses, const dlc::LearnerList& learner, int32_t n) {
+  for (int32_t a = 0; a < n_uses; ++a) {
+    for (int32_t b = 0; b < a; ++b) {
+      if ((use[a].written || use[b].written) && !apart(use[a], use[b], learner, n))
+        return fail(DLC_ERR_INVALID_ARGUMENT, "the call's buffers must not overlap");
+    }
+  }
+  return DLC_OK;
+}
+
 int32_t check_float_type(int32_t type, const char* name, bool wide) {
   if (type == DLC_BFLOAT16 || type == DLC_FLOAT16 || (wide && type == DLC_FLOAT32)) return DLC_OK;
   return fail(DLC_ERR_INVALID_ARGUMENT, std::string(name) + " is not one of the call's types");
 }
+
+int32_t element_bytes(int32_t type) { return type == DLC_FLOAT32 ? 4 : 2; }
 
 // No C++ exception crosses the ABI: running out of host memory is an error code.
 template <typename F>
@@ -175,14 +233,26 @@ int32_t adamw_step(float* theta_learners, const void* grads, int32_t grad_type, 
   const void* buffers[] = {theta_learners, grads, mo.m, mo.v, mo.m_scales, mo.v_scales, working};
   for (const void* p : buffers) {
     if (!aligned256(p)) return fail(DLC_ERR_ALIGNMENT, "device pointers must be 256-byte aligned");
-    if (p && std::count(std::begin(buffers), std::end(buffers), p) > 1)
-      return fail(DLC_ERR_INVALID_ARGUMENT, "the call's buffers must not overlap");
   }
   if (!aligned8(steps) || !aligned8(grad_scale) || !aligned8(lr_scale))
     return fail(DLC_ERR_ALIGNMENT, "steps, grad_scale and lr_scale must be 8-byte aligned");
   rc = check_float_type(grad_type, "grad_type", true);
   if (rc == DLC_OK && working) rc = check_float_type(working_type, "working_type", false);
   if (rc == DLC_OK) rc = check_tensors(tensors, n_tensors, learner_stride, true);
+  if (rc != DLC_OK) return rc;
+  const RowSpan span(tensors, n_tensors);
+  const int64_t moment = mo.coded ? 1 : 4;
+  const Use uses[] = {span.rows(theta_learners, learner_stride, 4, true),
+                      span.rows(grads, learner_stride, element_bytes(grad_type), false),
+                      span.rows(mo.m, learner_stride, moment, true),
+                      span.rows(mo.v, learner_stride, moment, true),
+                      span.scales(mo.m_scales, learner_stride),
+                      span.scales(mo.v_scales, learner_stride),
+                      span.rows(working, learner_stride, 2, true),
+                      per_learner(steps, true),
+                      per_learner(grad_scale, false),
+                      per_learner(lr_scale, false)};
+  rc = check_apart(uses, (int32_t)(sizeof(uses) / sizeof(uses[0])), a.learner, a.n_present);
   if (rc != DLC_OK) return rc;
   if (!groups || n_groups < 1 || n_groups > DLC_MAX_GROUPS)
     return fail(DLC_ERR_INVALID_ARGUMENT, "groups must hold 1 to 16 groups");
@@ -259,7 +329,6 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
     if (rc != DLC_OK) return rc;
     if (!grads || !norm || !grad_scale)
       return fail(DLC_ERR_INVALID_ARGUMENT, "grads, norm and grad_scale must not be NULL");
-    if (norm == grad_scale) return fail(DLC_ERR_INVALID_ARGUMENT, "the call's buffers must not overlap");
     if (!aligned256(grads)) return fail(DLC_ERR_ALIGNMENT, "device pointers must be 256-byte aligned");
     if (!aligned8(norm) || !aligned8(grad_scale))
       return fail(DLC_ERR_ALIGNMENT, "norm and grad_scale must be 8-byte aligned");
@@ -270,11 +339,16 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
       return fail(DLC_ERR_INVALID_ARGUMENT, "unscale must be finite and > 0");
     if (!(max_norm > 0.0)) return fail(DLC_ERR_INVALID_ARGUMENT, "max_norm must be > 0");
     const std::vector<Range> ranges = join_tensors(tensors, n_tensors, nullptr);
-    const InnerPartition p = norm_partition(ranges, grad_type == DLC_FLOAT32 ? 4 : 2);
+    const InnerPartition p = norm_partition(ranges, element_bytes(grad_type));
     const size_t need = round256((size_t)p.n_slots * a.n_present * sizeof(double));
     if (workspace == nullptr || workspace_bytes < need)
       return fail(DLC_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
     if (!aligned256(workspace)) return fail(DLC_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+    const Use uses[] = {RowSpan(tensors, n_tensors).rows(grads, learner_stride, element_bytes(grad_type), false),
+                        per_learner(norm, true), per_learner(grad_scale, true),
+                        {reinterpret_cast<uintptr_t>(workspace), 0, need, true}};
+    rc = check_apart(uses, (int32_t)(sizeof(uses) / sizeof(uses[0])), a.learner, a.n_present);
+    if (rc != DLC_OK) return rc;
     a.grads = grads;
     a.stride = learner_stride;
     a.part = static_cast<double*>(workspace);

@@ -493,8 +493,8 @@ int32_t dlc_rda_outer_step(float* theta_global, float* momentum, const float* th
  *   norm, grad_scale  device fp64 [n_learners], written for present learners
  *   workspace   >= dlc_grad_norm_workspace_bytes(n_learners, tensors, n_tensors)
  *               bytes, 256-byte aligned, no initial contents required
- * The sum's order depends on the tensor list and grad_type alone: repeated calls agree
- * bit for bit.
+ * No two of these buffers may overlap (as in dlc_adamw_step below).  The sum's order depends
+ * on the tensor list and grad_type alone: repeated calls agree bit for bit.
  */
 int32_t dlc_grad_norm_workspace_bytes(int32_t n_learners, const dlc_tensor* tensors, int32_t n_tensors,
                                       size_t* bytes);
@@ -534,8 +534,10 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
  *               when the call runs (a replayed graph follows the schedule)
  *   working     device [n_learners][learner_stride] of working_type (DLC_BFLOAT16 or
  *               DLC_FLOAT16), or NULL (working_type is then ignored)
- * The buffers must not overlap.  Device pointers 256-byte aligned, except steps,
- * grad_scale and lr_scale: 8-byte aligned.
+ * No buffer that is written may overlap another in what the call uses of them (present
+ * learners' entries, and of their rows the stretch from the first tensor to the last):
+ * DLC_ERR_INVALID_ARGUMENT.  Device pointers 256-byte aligned, except steps, grad_scale and
+ * lr_scale: 8-byte aligned.
  */
 typedef struct dlc_adamw_group {
     double lr, beta1, beta2, eps, weight_decay;

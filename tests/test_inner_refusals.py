@@ -1,0 +1,61 @@
+"""Calls of the learners' inner step that look right argument by argument and are not: refused before
+anything reaches the device.  Addresses of the C calls are never dereferenced.  The same tests run
+once more against the library with its host code under the sanitizers."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+import diloco_outer_step_amd as dlc
+from tests.test_host_sanitizers import CLANG, ROOT, asan_runtime, hostsan_library
+from tests.test_inner_host import F, INVALID, norm, step
+
+ROW = 4096  # elements of a row in the calls below; two learners
+
+
+# --- buffers that overlap ----------------------------------------------------------------
+
+@pytest.mark.parametrize("coded", [False, True])
+@pytest.mark.parametrize("bad", [
+    dict(m=F[0] + 4 * ROW),                          # the moments' first row is theta's second
+    dict(theta=F[2] + 256),
+    dict(m=F[3] - 256),                              # the end of one row, the start of another buffer
+    dict(grads=F[0] + 2 * 4 * ROW - 256),            # the last elements of the last row
+    dict(grads=F[2] + 512, gt=1),                    # 16-bit rows within wider ones
+    dict(work=F[0] + 256), dict(work=F[1] + 4 * ROW + 2 * ROW), dict(work=F[3] + 256, wt=2),
+    dict(steps=F[0] + 8), dict(steps=F[1] + 2 * 4 * ROW - 8),
+    dict(gs=F[6]), dict(gs=F[6] + 8), dict(gs=F[6] - 8), dict(lrs=F[6]), dict(lrs=F[6] - 8),
+    dict(gs=F[0] + 4 * ROW), dict(lrs=F[3] + 64),
+    dict(present=[0, 1], k=2, grads=F[0] + 256),
+])
+def test_adamw_refuses_buffers_that_overlap_by_an_offset(coded, bad):
+    assert step(coded, **bad) == INVALID and "overlap" in dlc.dlc_last_error()
+
+
+@pytest.mark.parametrize("bad", [
+    dict(ms=F[2] + 256), dict(vs=F[2] + 2 * ROW - 256), dict(vs=F[4] - 0), dict(ms=F[0] + 1024), dict(vs=F[5], ms=F[5]),
+    dict(steps=F[4] + 64), dict(gs=F[5] + 8), dict(m=F[4] - 256),
+])
+def test_the_coded_step_refuses_scale_bytes_that_overlap(bad):
+    assert step(True, **bad) == INVALID and "overlap" in dlc.dlc_last_error()
+
+
+@pytest.mark.parametrize("bad", [
+    dict(scale=F[1] + 8), dict(out=F[2] + 8), dict(ws=F[0]), dict(ws=F[0] + 4 * ROW), dict(out=F[3] + 8),
+    dict(scale=F[3]), dict(out=F[0] + 800), dict(scale=F[0] + 2 * 4 * ROW - 8), dict(ws=F[1]), dict(ws=F[2]),
+])
+def test_the_norm_refuses_buffers_that_overlap(bad):
+    assert norm(**bad) == INVALID and "overlap" in dlc.dlc_last_error()
+
+
+@pytest.mark.skipif(not os.path.exists(CLANG) or asan_runtime() is None,
+                    reason="ROCm clang with the sanitizer runtimes is not installed")
+@pytest.mark.skipif("DLC_LIBRARY" in os.environ, reason="already under the sanitizers")
+def test_these_tests_under_the_sanitizers():
+    env = dict(os.environ, LD_PRELOAD=asan_runtime(), DLC_LIBRARY=hostsan_library(),
+               ASAN_OPTIONS="detect_leaks=0:halt_on_error=1", UBSAN_OPTIONS="print_stacktrace=1")
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", "-m", "not gpu", __file__],
+                       capture_output=True, text=True, timeout=900, env=env, cwd=ROOT)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
+    assert "Sanitizer" not in r.stderr and "runtime error" not in r.stderr, r.stderr[-3000:]
