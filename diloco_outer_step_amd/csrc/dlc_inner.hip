@@ -296,23 +296,25 @@ __device__ __forceinline__ uint64_t next_step(const AdamWArgs& a, int i, const L
 }
 
 // theta - (eta wd theta + step).  The hardware's square root and reciprocal are within
-// one unit in the last place but take no subnormal operand: kTinyV scales a tiny v up.
-// m may be subnormal, so it is divided before it is scaled.
+// one unit in the last place but take no subnormal operand: with tiny_v a v below 2^-96 is
+// scaled up.  m may be subnormal, so it is divided before it is scaled.
 // Error, in units of 2^-24 of the step: size 5 (eta, the correction, its reciprocal 2, the
-// product), root 2.5, the square root 2, the denominator's sum and eps 1, its reciprocal 2,
-// two products 2: 14.5, below 2^-20 in all; the sum with the decay adds half a step of its own.
-template <bool kTinyV>
-__device__ __forceinline__ float new_theta(const Rates& r, float theta, float m, float v) {
-  const bool tiny = kTinyV && v < 0x1p-96f;
+// product), root 2.5, the square root 2, the denominator's sum and eps 1, a subnormal v left
+// out 1/8, the reciprocal 2, two products 2: 14.6, below 2^-20 in all; the sum with the
+// decay adds half a step of its own.
+__device__ __forceinline__ float new_theta(const Rates& r, float theta, float m, float v, bool tiny_v) {
+  const bool tiny = tiny_v && v < 0x1p-96f;
   float s = __builtin_amdgcn_sqrtf(tiny ? v * 0x1p64f : v);
-  if (kTinyV) s *= tiny ? 0x1p-32f : 1.0f;
+  s *= tiny ? 0x1p-32f : 1.0f;
   const float q = m * __builtin_amdgcn_rcpf(__fmaf_rn(s, r.root, r.eps));
   return theta - __fmaf_rn(r.shrink, theta, r.size * q);
 }
 
-// A subnormal v taken as 0 changes the denominator by less than 2^-63 root: nothing next
-// to an eps of 2^-40 root (9e-13 of it; eps is 1e-8 by default, root 32 at the most).
-__device__ __forceinline__ bool tiny_v_matters(const Rates& r) { return r.eps < r.root * 0x1p-40f; }
+// A subnormal v taken as 0 lowers the denominator by less than 2^-63 root: 2^-27 of itself
+// at most next to an eps of 2^-36 root (4.6e-10 where root is 32; eps is 1e-8 by default).
+// The rule looks at the group and the step alone, not at where in a tile an element lies, so
+// the result does not depend on how tensors are joined or split.
+__device__ __forceinline__ bool tiny_v_matters(const Rates& r) { return r.eps < r.root * 0x1p-36f; }
 
 template <typename G, typename W>
 __global__ __launch_bounds__(kAdamWBlock) void k_adamw(const AdamWArgs a, const InnerGeom g) {
@@ -339,19 +341,20 @@ __global__ __launch_bounds__(kAdamWBlock) void k_adamw(const AdamWArgs a, const 
   else load(n);
   if (!takes_step(l.clip)) return;
   const Rates r = rates_of(a.group[s.group], l.clip, l.lr_scale, next_step(a, i, l));
+  const bool tiny_v = tiny_v_matters(r);
   const auto finish = [&](auto fast, int n) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       mm[c] = new_m(r.b1, r.c1, mm[c], gr.value(c));
       vv[c] = new_v(r.b2, r.c2, vv[c], gr.value(c));
-      th[c] = new_theta<!decltype(fast)::value>(r, th[c], mm[c], vv[c]);
+      th[c] = new_theta(r, th[c], mm[c], vv[c], !decltype(fast)::value && tiny_v);
     }
     store4(theta + at, n, th);
     store4(m + at, n, mm);
     store4(v + at, n, vv);
     if constexpr (!std::is_void_v<W>) store4((W*)a.working + row + at, n, th);
   };
-  if (full && !tiny_v_matters(r)) finish(std::true_type(), 4);
+  if (full && !tiny_v) finish(std::true_type(), 4);
   else finish(std::false_type(), n);
 }
 
@@ -501,6 +504,7 @@ __global__ __launch_bounds__(kCodedBlock) void k_adamw_coded(const AdamWArgs a, 
   const uint64_t t = next_step(a, i, l);
   const Rates r = rates_of(a.group[s.group], l.clip, l.lr_scale, t);
   const Keys first = keys_of(a.seed, t, i, (uint32_t)(s.base >> 32));
+  const bool tiny_v = tiny_v_matters(r);
   const auto finish = [&](auto fast) {
     constexpr bool kFast = decltype(fast)::value;
 #pragma unroll
@@ -519,7 +523,7 @@ __global__ __launch_bounds__(kCodedBlock) void k_adamw_coded(const AdamWArgs a, 
       for (int c = 0; c < 4; ++c) {
         mm[c] = new_m(b1, r.c1, mm[c], gr[j].value(c));
         vv[c] = new_v(b2, r.c2, vv[c], gr[j].value(c));
-        th[j][c] = new_theta<!kFast>(r, th[j][c], mm[c], vv[c]);
+        th[j][c] = new_theta(r, th[j][c], mm[c], vv[c], !kFast && tiny_v);
         if (c >= n) mm[c] = vv[c] = 0.0f;  // not the tensor's: no part of the block's maximum
       }
       // every lane of a step takes part in its block's maximum
@@ -563,7 +567,7 @@ __global__ __launch_bounds__(kCodedBlock) void k_adamw_coded(const AdamWArgs a, 
     }
   };
   // a block past a multiple of 2^32 elements has two sets of keys: the general path's case
-  if (full && !tiny_v_matters(r) && (uint32_t)s.base + kCodedTile > (uint32_t)s.base) finish(std::true_type());
+  if (full && !tiny_v && (uint32_t)s.base + kCodedTile > (uint32_t)s.base) finish(std::true_type());
   else finish(std::false_type());
 }
 

@@ -19,6 +19,9 @@ from tests import test_gpu_inner as base
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+# Neighbours without padding, so that a call of the whole list has one range (and a last one apart), whose
+# tiles of 256 and of 1024 elements end inside of tensors; one by one most of them end in a partial tile.
+JOINED = [64 * 3, 64 * 5, 64 * 16, 64, 64 * 37, 64 * 64, 64 * 2, 64 * 15, 100]
 
 
 def moments_of(coded):
@@ -103,3 +106,56 @@ def test_what_is_only_read_may_be_shared_and_small_arrays_may_touch():
     torch.cuda.synchronize()
     for n in ("theta", "m", "v", "steps"):
         assert torch.equal(a[n], b[n]), n
+
+
+# --- how the tensors are split -----------------------------------------------------------
+
+def split_three_ways(b, tensors, coded, group):
+    """The step of the whole list, of the tensors one by one, of the list in another order: bit for bit alike."""
+    start = clone(b)
+    step(b, tensors, coded, group)
+    for parts in ([[t] for t in tensors[::-1]], [tensors[1::2] + tensors[::2]]):
+        c = clone(start)
+        for part in parts:
+            c["steps"].copy_(start["steps"])
+            step(c, part, coded, group)
+        torch.cuda.synchronize()
+        for n in ("theta", "steps") + moments_of(coded):
+            same = torch.equal(b[n].view(torch.uint8), c[n].view(torch.uint8))
+            assert same, (n, len(parts), int((b[n] != c[n]).sum()))
+    return start
+
+
+@pytest.mark.parametrize("coded", [False, True])
+@pytest.mark.parametrize("grads", ["fp32", "bf16"])
+def test_results_do_not_depend_on_how_joined_tensors_are_split(coded, grads):
+    tensors, stride = base.layout(JOINED)
+    split_three_ways(state(2, stride, tensors, grads), tensors, coded, dlc.AdamWGroup(1e-3, 0.9, 0.999, 1e-8, 0.1))
+
+
+# root = 1 / sqrt(1 - beta2^t) is 31.6 at the first step and 1 at a late one: eps on both sides of 2^-40 root and
+# of 2^-36 root, the default, and the smallest
+@pytest.mark.parametrize("coded", [False, True])
+@pytest.mark.parametrize("eps", [1e-8, 4.7e-10, 4.5e-10, 3e-11, 1.5e-11, 1.4e-11, 1e-12, 9e-13, 1e-18, 1.2e-38])
+@pytest.mark.parametrize("steps", [0, 1_000_000])
+def test_tiny_second_moments_whatever_the_split(coded, eps, steps):
+    tensors, stride = base.layout(JOINED)
+    b = state(2, stride, tensors)
+    b["steps"].fill_(steps)
+    gen = torch.Generator().manual_seed(5)
+    b["grads"] = (torch.randn(b["grads"].shape, generator=gen) * 3e-18).to(DEV)  # v is about 1e-38
+    if coded:
+        for n in moments_of(True):
+            b[n].zero_()
+    else:
+        b["v"] = (torch.rand(b["v"].shape, generator=gen) * 2e-38).to(DEV)
+        b["m"] = (torch.randn(b["m"].shape, generator=gen) * min(1.0, eps)).to(DEV)
+    b["theta"].mul_(1e-6)  # the step's last bits show in theta
+    group = dlc.AdamWGroup(1e-6, 0.9, 0.999, eps, 0.1)
+    start = split_three_ways(b, tensors, coded, group)
+    r = {n: base.host(start[n]).copy() for n in ("theta", "steps") + moments_of(coded)}
+    size = oracle_step(r, base.host(start["grads"]), tensors, coded, [group])
+    base.near_theta(base.host(b["theta"]), r["theta"], size, b["mask"], "theta")
+    for n in moments_of(coded):
+        base.same(np.where(b["mask"], base.host(b[n]), 0) if b[n].shape == b["theta"].shape else base.host(b[n]),
+                  np.where(b["mask"], r[n], 0) if b[n].shape == b["theta"].shape else r[n], n)
