@@ -262,8 +262,9 @@ int32_t adamw_step(float* theta_learners, const void* grads, int32_t grad_type, 
       return fail(DLC_ERR_INVALID_ARGUMENT, "lr and weight_decay must be finite and >= 0");
     if (!(s.beta1 >= 0.0 && s.beta1 < 1.0 && s.beta2 >= 0.0 && s.beta2 < 1.0))
       return fail(DLC_ERR_INVALID_ARGUMENT, "betas must be in [0, 1)");
-    if (!(s.eps >= FLT_MIN && s.eps <= FLT_MAX))
-      return fail(DLC_ERR_INVALID_ARGUMENT, "eps must be a normal positive fp32 number");
+    // Past 2^126 the reciprocal of the update's denominator would be subnormal, which the hardware's gives as 0.
+    if (!(s.eps >= FLT_MIN && s.eps <= 0x1p126))
+      return fail(DLC_ERR_INVALID_ARGUMENT, "eps must be in [2^-126, 2^126]");
     a.group[q] = {s.lr, s.beta1, s.beta2, s.eps, s.weight_decay, std::log(s.beta1), std::log(s.beta2)};
   }
   if (group_of) {

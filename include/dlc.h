@@ -515,7 +515,8 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
  *   working <- theta rounded to working_type (nearest even)
  *   steps[i] <- t
  * m and v are computed in fp64 and rounded to fp32 once; the change of theta is an
- * fp32 expression of the rounded moments, within 2^-20 of its two terms' magnitudes,
+ * fp32 expression of the rounded moments, within 2^-20 of its two terms' magnitudes
+ * as long as eta, eta / (1 - beta1^t) and m's quotient are normal fp32 numbers or 0,
  * and is subtracted with one rounding.
  *   theta_learners  device fp32 [n_learners][learner_stride], updated in place
  *   grads       as dlc_grad_norm
@@ -525,7 +526,7 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
  *               up by the call.  It belongs to the call's tensors: a model stepped in several
  *               calls keeps one array for each.
  *   groups      host [n_groups], 1..DLC_MAX_GROUPS; lr and weight_decay finite and
- *               >= 0, betas in [0, 1), eps a normal positive fp32 number
+ *               >= 0, betas in [0, 1), eps in [2^-126, 2^126]
  *   group_of    host int32 [n_tensors]: group of each tensor; NULL = all group 0
  *   grad_scale  device fp64 [n_learners], or NULL = 1.  A learner whose entry is not
  *               finite and > 0 is left out: nothing of it is written, its step is

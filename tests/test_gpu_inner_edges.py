@@ -159,3 +159,19 @@ def test_tiny_second_moments_whatever_the_split(coded, eps, steps):
     for n in moments_of(coded):
         base.same(np.where(b["mask"], base.host(b[n]), 0) if b[n].shape == b["theta"].shape else base.host(b[n]),
                   np.where(b["mask"], r[n], 0) if b[n].shape == b["theta"].shape else r[n], n)
+
+
+# --- eps at the upper end ------------------------------------------------------------------
+
+@pytest.mark.parametrize("eps", [2.0 ** 126, 2.0 ** 126 * (1 - 2.0 ** -24), 1e30])
+def test_the_largest_eps(eps):
+    tensors, stride = base.layout([1, 65, 4099, 256])
+    b = state(2, stride, tensors)
+    b["m"].mul_(2.0 ** 120)
+    group = dlc.AdamWGroup(1.0, 0.9, 0.999, eps, 0.0)
+    r = {n: base.host(b[n]).copy() for n in ("theta", "steps", "m", "v")}
+    step(b, tensors, False, group)
+    torch.cuda.synchronize()
+    size = oracle_step(r, base.host(b["grads"]), tensors, False, [group])
+    assert size[b["mask"]].max() > 1e-6
+    base.near_theta(base.host(b["theta"]), r["theta"], size, b["mask"], "theta")

@@ -49,6 +49,15 @@ def test_the_norm_refuses_buffers_that_overlap(bad):
     assert norm(**bad) == INVALID and "overlap" in dlc.dlc_last_error()
 
 
+# --- eps -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("coded", [False, True])
+@pytest.mark.parametrize("eps", [2.0 ** 126 * (1 + 2.0 ** -52), 2.0 ** 127, 3.4e38, 1e300, float("inf"), float("nan"),
+                                 2.0 ** -126 * (1 - 2.0 ** -53)])
+def test_adamw_refuses_an_eps_whose_reciprocal_is_not_a_normal_number(coded, eps):
+    assert step(coded, groups=((1e-3, 0.9, 0.999, eps, 0.0),)) == INVALID and "eps" in dlc.dlc_last_error()
+
+
 @pytest.mark.skipif(not os.path.exists(CLANG) or asan_runtime() is None,
                     reason="ROCm clang with the sanitizer runtimes is not installed")
 @pytest.mark.skipif("DLC_LIBRARY" in os.environ, reason="already under the sanitizers")
