@@ -772,6 +772,8 @@ def _adamw(theta_L, grads, moments, steps, tensors, groups, group_of, grad_scale
     ids = None
     if group_of is not None:
         ids = group_ids(group_of)
+        if ids is group_of:  # the library reads it while other threads run: not the caller's own array
+            ids = ids[:]
         if len(ids) != len(tensors):
             raise ValueError(f"group_of holds {len(ids)} values for {len(tensors)} tensors")
     _check_buffers(bufs)

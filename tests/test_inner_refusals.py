@@ -1,11 +1,13 @@
 """Calls of the learners' inner step that look right argument by argument and are not: refused before
 anything reaches the device.  Addresses of the C calls are never dereferenced.  The same tests run
 once more against the library with its host code under the sanitizers."""
+import ctypes
 import os
 import subprocess
 import sys
 
 import pytest
+import torch
 
 import diloco_outer_step_amd as dlc
 from tests.test_host_sanitizers import CLANG, ROOT, asan_runtime, hostsan_library
@@ -56,6 +58,44 @@ def test_the_norm_refuses_buffers_that_overlap(bad):
                                  2.0 ** -126 * (1 - 2.0 ** -53)])
 def test_adamw_refuses_an_eps_whose_reciprocal_is_not_a_normal_number(coded, eps):
     assert step(coded, groups=((1e-3, 0.9, 0.999, eps, 0.0),)) == INVALID and "eps" in dlc.dlc_last_error()
+
+
+# --- the binding -----------------------------------------------------------------------------
+
+def arguments(monkeypatch, during=lambda args: None):
+    """An AdamW call on host tensors that stops before the library: what reaches it. `during` runs in its place."""
+    seen = []
+
+    def library(*args):
+        during(args)
+        seen.append(args)
+        return 0
+
+    monkeypatch.setattr(dlc, "_check_buffers", lambda bufs: None)
+    monkeypatch.setattr(dlc, "_on_device", lambda index, stream, fn, *args: library(*args))
+
+    def call(tensors, **kw):
+        z = [torch.zeros((2, 256)) for _ in range(4)]
+        dlc.dlc_adamw_step(*z, torch.zeros(2, dtype=torch.int64), tensors, **kw)
+        return seen[-1]
+
+    return call
+
+
+def test_the_library_reads_group_ids_that_no_other_thread_can_change(monkeypatch):
+    ids = dlc.group_ids([0, 1])
+    own = ids.buffer_info()[0]
+
+    def another_thread():  # ctypes has released the interpreter's lock by then
+        ids[1] = 7
+        ids.extend([7] * 100_000)  # moves the array's items
+
+    read = []
+    call = arguments(monkeypatch, lambda args: (another_thread(), read.extend((ctypes.c_int32 * 2).from_address(args[11]))))
+    q = dlc.AdamWGroup()
+    args = call([(0, 0, 64), (64, 64, 64)], groups=[q, q], group_of=ids)
+    assert read == [0, 1] and args[11] != own
+    assert len(ids) == 100_002
 
 
 @pytest.mark.skipif(not os.path.exists(CLANG) or asan_runtime() is None,
