@@ -81,6 +81,9 @@ class AdamWGroup(NamedTuple):
     weight_decay: float = 0.01
 
 
+_GROUP_FIELDS = len(AdamWGroup._fields)
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python diloco_outer_step_amd/build.py`")
@@ -766,9 +769,10 @@ def _adamw(theta_L, grads, moments, steps, tensors, groups, group_of, grad_scale
         bufs.append(("working", working, working.dtype, rows))
     if isinstance(groups, AdamWGroup):
         groups = (groups,)
+    for q in groups:
+        if len(q) != _GROUP_FIELDS:
+            raise ValueError("groups must hold AdamWGroup entries")
     gs = array.array("d", itertools.chain.from_iterable(groups))
-    if len(gs) != len(AdamWGroup._fields) * len(groups):
-        raise ValueError("groups must hold AdamWGroup entries")
     ids = None
     if group_of is not None:
         ids = group_ids(group_of)

@@ -98,6 +98,21 @@ def test_the_library_reads_group_ids_that_no_other_thread_can_change(monkeypatch
     assert len(ids) == 100_002
 
 
+@pytest.mark.parametrize("groups", [
+    [(1e-3, 0.9, 0.999, 1e-8), (0.1, 1e-3, 0.9, 0.999, 1e-8, 0.1)],  # ten values, in two entries of the wrong lengths
+    [(1e-3, 0.9, 0.999, 1e-8, 0.1, 0.0)] * 5, [(1e-3,)] * 5, [()],
+])
+def test_every_group_holds_its_five_values(monkeypatch, groups):
+    with pytest.raises(ValueError, match="AdamWGroup"):
+        arguments(monkeypatch)([(0, 0, 64)], groups=groups)
+
+
+def test_groups_as_a_single_one_as_a_list_and_as_plain_tuples(monkeypatch):
+    call, q = arguments(monkeypatch), dlc.AdamWGroup(0.5, 0.25, 0.125, 1e-8, 2.0)
+    for groups, n in ((q, 1), ([q], 1), ((tuple(q), list(q)), 2), ([q] * 16, 16)):
+        assert call([(0, 0, 64)], groups=groups)[13] == n
+
+
 @pytest.mark.skipif(not os.path.exists(CLANG) or asan_runtime() is None,
                     reason="ROCm clang with the sanitizer runtimes is not installed")
 @pytest.mark.skipif("DLC_LIBRARY" in os.environ, reason="already under the sanitizers")
