@@ -151,7 +151,7 @@ class TensorList(tuple):
     list at every step)."""
 
     def __new__(cls, tensors: Sequence[Tuple[int, int, int]]):
-        self = super().__new__(cls, tensors)
+        self = super().__new__(cls, [(offset, loffset, numel) for offset, loffset, numel in tensors])
         plain = tuple(self)
         self._c, self._ends = _tensors(plain), (0, 0)
         if plain:

@@ -113,6 +113,22 @@ def test_groups_as_a_single_one_as_a_list_and_as_plain_tuples(monkeypatch):
         assert call([(0, 0, 64)], groups=groups)[13] == n
 
 
+@pytest.mark.parametrize("tensors", [
+    [(0, 0, 64, 7), (64, 64, 64, 7), (128, 128, 64, 7)], [(0, 0), (64, 64, 64, 64)], [(0, 0)], [()], [0, 0, 64],
+])
+def test_every_entry_of_a_tensor_list_holds_three_values(tensors):
+    with pytest.raises((ValueError, TypeError)):
+        dlc.TensorList(tensors)
+
+
+def test_a_tensor_list_does_not_follow_its_source():
+    rows = [[0, 0, 64], [64, 64, 64]]
+    t = dlc.TensorList(rows)
+    rows[1][2] = 1 << 20
+    assert list(t) == [(0, 0, 64), (64, 64, 64)] and dlc._extents(t) == (128, 128)
+    assert dlc._tensors(t)[0][1].numel == 64
+
+
 @pytest.mark.skipif(not os.path.exists(CLANG) or asan_runtime() is None,
                     reason="ROCm clang with the sanitizer runtimes is not installed")
 @pytest.mark.skipif("DLC_LIBRARY" in os.environ, reason="already under the sanitizers")
