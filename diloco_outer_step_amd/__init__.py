@@ -159,6 +159,9 @@ class TensorList(tuple):
             self._ends = tuple(int(x) for x in (a[:, :2] + a[:, 2:]).max(0))
         return self
 
+    def __reduce__(self):  # pickled and copied as the triples: the C structs are made anew
+        return type(self), (tuple(self),)
+
 
 def _tensors(tensors: Sequence[Tuple[int, int, int]]):
     """dlc_tensor array of (offset, loffset, numel) triples: one int64 [n][3] array

@@ -2,7 +2,9 @@
 anything reaches the device.  Addresses of the C calls are never dereferenced.  The same tests run
 once more against the library with its host code under the sanitizers."""
 import ctypes
+import copy
 import os
+import pickle
 import subprocess
 import sys
 
@@ -127,6 +129,15 @@ def test_a_tensor_list_does_not_follow_its_source():
     rows[1][2] = 1 << 20
     assert list(t) == [(0, 0, 64), (64, 64, 64)] and dlc._extents(t) == (128, 128)
     assert dlc._tensors(t)[0][1].numel == 64
+
+
+@pytest.mark.parametrize("tensors", [[], [(0, 0, 100), (128, 192, 70)]])
+def test_a_tensor_list_can_be_pickled_and_copied(tensors):
+    t = dlc.TensorList(tensors)
+    for again in (pickle.loads(pickle.dumps(t)), copy.copy(t), copy.deepcopy(t)):
+        assert type(again) is dlc.TensorList and again == t and dlc._extents(again) == dlc._extents(t)
+        (arr, n), (want, _) = dlc._tensors(again), dlc._tensors(t)
+        assert n == len(tensors) and bytes(arr) == bytes(want)
 
 
 @pytest.mark.skipif(not os.path.exists(CLANG) or asan_runtime() is None,
