@@ -175,3 +175,93 @@ def test_the_largest_eps(eps):
     size = oracle_step(r, base.host(b["grads"]), tensors, False, [group])
     assert size[b["mask"]].max() > 1e-6
     base.near_theta(base.host(b["theta"]), r["theta"], size, b["mask"], "theta")
+
+
+# --- what lies behind a tensor -------------------------------------------------------------
+
+@pytest.mark.parametrize("coded", [False, True])
+@pytest.mark.parametrize("grads", ["fp32", "bf16", "fp16"])
+def test_padding_that_is_not_finite_has_no_influence_and_stays(coded, grads):
+    tensors, stride = base.layout(base.LISTS["ragged"])
+    clean = state(2, stride, tensors, grads)
+    clean["work"] = torch.zeros((2, stride), dtype=torch.bfloat16, device=DEV)
+    b = clone(clean)
+    outside = torch.from_numpy(~clean["mask"]).to(DEV)
+    for n in ("theta", "grads", "m", "v", "work"):
+        b[n][outside] = math.nan
+        b[n][outside & (torch.arange(stride, device=DEV) % 3 == 1)] = math.inf
+    b["mc"][outside], b["vc"][outside] = 0x7F, 0x7C
+    before = clone(b)
+    for x in (clean, b):
+        for _ in range(2):
+            step(x, tensors, coded, dlc.AdamWGroup(), working=x["work"])
+    torch.cuda.synchronize()
+    whole = torch.from_numpy(clean["mask"]).to(DEV)
+    for n in ("theta", "work") + (("mc", "vc") if coded else ("m", "v")):
+        assert torch.equal(b[n][whole], clean[n][whole]), n
+        raw = torch.uint8 if b[n].element_size() == 1 else torch.int16 if b[n].element_size() == 2 else torch.int32
+        assert torch.equal(b[n].view(raw)[outside], before[n].view(raw)[outside]), n
+    if coded:
+        assert torch.equal(b["ms"], clean["ms"]) and torch.equal(b["vs"], clean["vs"])
+
+
+# --- learners left out, their factors -------------------------------------------------------
+
+@pytest.mark.parametrize("coded", [False, True])
+@pytest.mark.parametrize("scale", [0.0, -1.0, math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("name", ["around_a_block", "ragged"])  # the step counted by the blocks, by a kernel of its own
+def test_a_learner_whose_step_is_left_out_keeps_every_bit(coded, scale, name):
+    tensors, stride = base.layout(base.LISTS[name])
+    b = state(3, stride, tensors, "bf16")
+    b["work"] = torch.full((3, stride), 7.0, dtype=torch.bfloat16, device=DEV)
+    clip = [1.0, scale, 0.25]
+    start = clone(b)
+    step(b, tensors, coded, base.GROUPS[0], working=b["work"],
+         grad_scale=torch.tensor(clip, dtype=torch.float64, device=DEV))
+    torch.cuda.synchronize()
+    r = {n: base.host(start[n]).copy() for n in ("theta", "steps") + moments_of(coded)}
+    size = oracle_step(r, base.host(start["grads"]), tensors, coded, [base.GROUPS[0]], clip)
+    base.near_theta(base.host(b["theta"]), r["theta"], size, b["mask"], "theta")
+    assert b["steps"].tolist() == r["steps"].tolist() == [1, 40, 81]
+    for n in ("theta", "work") + moments_of(coded):
+        assert torch.equal(b[n][1].view(torch.uint8), start[n][1].view(torch.uint8)), n
+        if n in r and n != "theta":
+            base.same(base.host(b[n]), r[n], n)
+    assert not torch.equal(b["theta"][0], start["theta"][0]) and not torch.equal(b["theta"][2], start["theta"][2])
+
+
+# --- the norm's one-block form --------------------------------------------------------------
+
+@pytest.mark.parametrize("grads", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("sizes", [[65] * 8, [65] * 9, [1] * 8, [1 << 16], [(1 << 16) - 64, 64], [(1 << 16) + 1],
+                                   [(1 << 13) - 3] * 8, [(1 << 13) + 1] * 8])
+def test_norm_on_both_sides_of_the_one_block_forms_limits(grads, sizes):
+    base.check_norm(sizes, grads, [1, 1, 0], 0.5, 1e-2)
+
+
+# --- codes -------------------------------------------------------------------------------------
+
+# exponents of the largest gradient of a block: m is the gradient itself (beta1 = 0), v its square (beta2 = 0)
+WINDOWS = [(-148, -121), (-121, -64), (-64, -50), (-50, 0), (0, 63), (63, 127)]
+
+
+@pytest.mark.parametrize("low,high", WINDOWS)
+def test_every_range_of_exponents_is_coded_as_defined(low, high):
+    """2^21 values of each window, each up to 2^26 below its block's largest: normal and subnormal codes, scale bytes
+    from 0 to the end, values below the code's grid, subnormal fp32 moments, second moments past fp32's end."""
+    n = 1 << 21
+    rng = np.random.default_rng(200 + high)
+    top = rng.integers(low, high, n // 64, endpoint=True).astype(np.float64)
+    e = np.repeat(top, 64) - np.where(np.arange(n) % 64 == 0, 0, rng.integers(0, 26, n, endpoint=True))
+    g = (np.exp2(np.minimum(e, 126)) * rng.uniform(1, 2, n) * rng.choice([-1, 1], n)).astype(np.float32)[None]
+    tensors = [(0, 0, n)]
+    group = (0.0, 0.0, 0.0, 1e-8, 0.0)
+    r = dict(theta=np.zeros((1, n), np.float32), mc=np.zeros((1, n), np.uint8), ms=np.zeros((1, n // 64), np.uint8),
+             vc=np.zeros((1, n), np.uint8), vs=np.zeros((1, n // 64), np.uint8), steps=np.full(1, high + 200, np.int64))
+    b = {name: torch.from_numpy(x.copy()).to(DEV) for name, x in r.items()}
+    b["grads"] = torch.from_numpy(g).to(DEV)
+    step(b, tensors, True, dlc.AdamWGroup(*group))
+    torch.cuda.synchronize()
+    oracle_step(r, g, tensors, True, [group])
+    for name in moments_of(True):
+        base.same(base.host(b[name]), r[name], name)
