@@ -4,8 +4,10 @@
 //
 //   k_norm_partial  sum of squares of a block's gradients, fp64
 //   k_norm_final    the blocks' sums in a fixed order -> norm and gradient scale
+//   k_norm_small    both in one block per learner, for short lists
 //   k_adamw         one pass over theta, the moments and the gradients
-//   k_adamw_advance the learners' step counts
+//   k_adamw_coded   the same with coded moments
+//   k_adamw_advance the learners' step counts, where k_adamw's blocks do not count them
 //
 // AdamW per element, with t = steps + 1, g = grad_scale * grad, eta = lr * lr_scale:
 //   m     <- beta1 m + (1 - beta1) g

@@ -103,7 +103,14 @@ InnerPartition norm_partition(const std::vector<Range>& ranges, int32_t bytes_pe
   return inner_partition(ranges, step * std::max<int64_t>(1, (steps + kNormBlocks - 1) / kNormBlocks));
 }
 
-// Few elements in few ranges: one block per learner does it all.
+// Few elements in few ranges: one block per learner does it all, and there is no second
+// launch.  One block against two kernels, us a call from Python / us a call replayed from a
+// graph (fp32, one learner; 16-bit gradients and eight learners are within 10%, but for 2^17 and
+// 2^18 elements):
+//   1 range    2^13: 8.7, 10.8 / 2.7, 4.1   2^16: 8.9, 11.1 / 4.5, 4.4   2^18: 11.7, 11.1 / 10.6, 4.5
+//   8 ranges   2^13: 9.0, 11.1 / 4.3, 4.3   2^16: 8.9, 11.1 / 5.9, 4.4   2^18: 13.2, 11.2 / 12.3, 4.5
+//   32 ranges  2^13: 11.4, 11.2 / 10.3, 4.3
+// The limits are the last place where no way of calling loses more than 1.5 us.
 constexpr int64_t kSmallNorm = 1 << 16, kSmallNormRanges = 8;
 
 bool small_norm(const std::vector<Range>& ranges) {
@@ -111,9 +118,16 @@ bool small_norm(const std::vector<Range>& ranges) {
 }
 
 // Calls of at most this many blocks per learner count the step in the AdamW kernel itself:
-// one launch less is 2.7 us less where the host's launches are the time (11.4 against
-// 14.1 us for four vectors), but tickets on one address pass at about 45 ns each (9100
-// of them: 431 us for a call that takes 31).
+// one launch less, at the price of a ticket a block on the learner's count.  Counted by the
+// blocks against by a kernel of its own, us a call from Python (fp32 gradients, 32-bit moments):
+//   1 learner   16 to 128 blocks: 10.1, 12.3
+//   8 learners  to 48 blocks: 10.1, 12.3   64: 10.3, 12.3   80: 11.6, 12.3   96: 13.1, 12.3   128: 16.0, 12.3
+//   16 learners to 32 blocks: 7.5, 9.9   64: 10.4, 10.0 (on another machine, as the next line)
+//   64 learners to 16 blocks: 7.5, 9.9   32: 9.5, 9.9   64: 25.5, 10.0
+// (coded, 8 learners: 64: 11.6, 13.3   80: 13.2, 13.4   96: 14.8, 13.9).  Replayed from a graph the extra
+// launch costs less: 64 blocks 3.6, 3.8 and 96 blocks 4.0, 3.8 with one learner, but with eight 16 blocks 4.5, 3.9
+// and 64 blocks 9.2, 4.1.  Far above the limit tickets are out of the question: 431 us
+// for a call of 9100 blocks that takes 31.
 constexpr int64_t kMaxTickets = 64;
 
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }

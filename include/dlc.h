@@ -523,16 +523,17 @@ int32_t dlc_grad_norm(const void* grads, int32_t grad_type, int64_t learner_stri
  *   exp_avg     device fp32 [n_learners][learner_stride]: m (start with zeros)
  *   exp_avg_sq  device fp32 [n_learners][learner_stride]: v, never negative
  *   steps       device int64 [n_learners]: steps taken so far (below 2^40), counted
- *               up by the call.  It belongs to the call's tensors: a model stepped in several
- *               calls keeps one array for each.
+ *               up by the call, and not to be read or written elsewhere while it runs (its high
+ *               bits may be in use).  It belongs to the call's tensors: a model stepped in
+ *               several calls keeps one array for each.
  *   groups      host [n_groups], 1..DLC_MAX_GROUPS; lr and weight_decay finite and
  *               >= 0, betas in [0, 1), eps in [2^-126, 2^126]
  *   group_of    host int32 [n_tensors]: group of each tensor; NULL = all group 0
  *   grad_scale  device fp64 [n_learners], or NULL = 1.  A learner whose entry is not
  *               finite and > 0 is left out: nothing of it is written, its step is
  *               not counted.
- *   lr_scale    device fp64 [n_learners], or NULL = 1: the schedule's factor, read
- *               when the call runs (a replayed graph follows the schedule)
+ *   lr_scale    device fp64 [n_learners], or NULL = 1: the schedule's factor, finite,
+ *               read when the call runs (a replayed graph follows the schedule)
  *   working     device [n_learners][learner_stride] of working_type (DLC_BFLOAT16 or
  *               DLC_FLOAT16), or NULL (working_type is then ignored)
  * No buffer that is written may overlap another in what the call uses of them (present
