@@ -47,6 +47,12 @@ DLC_BFLOAT16 = 1
 DLC_FLOAT16 = 2
 DLC_MAX_GROUPS = 16
 DLC_CODE_BLOCK = 64
+DLC_MAX_EXPERTS = 1024
+DLC_MAX_CHOICES = 64
+DLC_MAX_TOKENS = 1 << 24
+DLC_INT32 = 0
+DLC_INT64 = 1
+DLC_ACCUMULATE = 16
 
 EXPORTED = (
     "dlc_fragment_plan", "dlc_workspace_bytes", "dlc_quantize_range", "dlc_quantize_encode",
@@ -54,6 +60,8 @@ EXPORTED = (
     "dlc_cycle_workspace_bytes", "dlc_outer_cycle", "dlc_outer_cycle_lanes", "dlc_ring_workspace_bytes", "dlc_ring_outer_step",
     "dlc_rda_workspace_bytes", "dlc_rda_outer_step", "dlc_cycle_rda_workspace_bytes", "dlc_outer_cycle_rda",
     "dlc_grad_norm_workspace_bytes", "dlc_grad_norm", "dlc_adamw_step", "dlc_adamw_coded_step",
+    "dlc_expert_balance_workspace_bytes", "dlc_expert_balance", "dlc_expert_weights",
+    "dlc_outer_grad_norm_workspace_bytes", "dlc_outer_grad_norm", "dlc_merge_clipped_step",
     "dlc_last_error", "dlc_version",
 )
 
@@ -122,6 +130,13 @@ def _load() -> ctypes.CDLL:
                            vp, i32, vp],
         "dlc_adamw_coded_step": [vp, vp, i32, vp, vp, vp, vp, vp, i64, i32, vp, tp, i32, vp, vp,
                                  i32, ctypes.c_uint64, vp, vp, vp, i32, vp],
+        "dlc_expert_balance_workspace_bytes": [i32, i64, i32, ctypes.POINTER(sz)],
+        "dlc_expert_balance": [vp, i32, i64, i64, vp, i32, i64, i64, vp, i64, i32, vp, i64, i32, i32, ctypes.c_double,
+                               vp, vp, i64, vp, vp, i64, vp, i64, i64, vp, u32, vp, sz, vp],
+        "dlc_expert_weights": [vp, i64, i32, i32, vp, vp, vp, i32, vp, vp],
+        "dlc_outer_grad_norm_workspace_bytes": [tp, i32, ctypes.POINTER(sz)],
+        "dlc_outer_grad_norm": [vp, i64, i32, vp, vp, vp, tp, i32, ctypes.c_double, vp, vp, vp, sz, vp],
+        "dlc_merge_clipped_step": [vp, vp, vp, i64, i32, vp, vp, vp, vp, tp, i32, ctypes.c_double, ctypes.c_double, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -826,3 +841,180 @@ def dlc_adamw_coded_step(theta_L, grads, m_codes, m_scales, v_codes, v_scales, s
     _on_device(theta_L.get_device(), stream, _lib.dlc_adamw_coded_step, theta_L.data_ptr(), grads.data_ptr(), gt,
                m_codes.data_ptr(), m_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), steps.data_ptr(),
                stride, k, pres, arr, n, _items(ids), _items(gs), ng, int(seed), scale, lrs, work, wt)
+
+
+# ---------------------------------------------------------------------------
+# Mixtures of experts under the outer step
+# ---------------------------------------------------------------------------
+_CHOICE_TYPES = {torch.int32: DLC_INT32, torch.int64: DLC_INT64}
+_MASK_TYPES = (torch.bool, torch.uint8)
+
+
+def _view(t, name: str, dtypes, shape):
+    """Refuse a view whose last dimension is not dense: (t's strides in elements but the last)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {', '.join(map(str, dtypes))}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return strides[:-1]
+
+
+def dlc_expert_balance_workspace_bytes(n_learners: int, n_tokens: int, n_experts: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.dlc_expert_balance_workspace_bytes(int(n_learners), int(n_tokens), int(n_experts), ctypes.byref(out)))
+    return out.value
+
+
+def alloc_expert_balance_workspace(n_learners: int, n_tokens: int, n_experts: int, device="cuda") -> torch.Tensor:
+    nbytes = max(256, dlc_expert_balance_workspace_bytes(n_learners, n_tokens, n_experts))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def dlc_expert_balance(logits, choices, loss, counts, workspace, coef=1.0, mask=None, mean_probs=None,
+                       grad_logits=None, grad_scale=None, totals=None, accumulate=False, present=None, stream=None):
+    """The balance loss of every present learner's router, its gradient and the experts' counts.
+    logits: [K, T, E] fp32, bf16 or fp16; choices: the experts of each token, int32 or int64
+    [K, T, top] (outside [0, E): dropped); mask: bool or uint8 [K, T], false where a token
+    does not count.  Written: loss fp32 [K], counts int64 [K, E], and where given mean_probs fp32
+    [K, E], grad_logits like logits (added to with `accumulate`), totals int64 [K, E] (added to).
+    grad_scale: device fp64 [K], the factor of the gradient.  logits, choices, mask, grad_logits,
+    counts and totals may be views with a dense last dimension."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+        raise ValueError("logits must be a [K, T, E] tensor")
+    if not isinstance(choices, torch.Tensor) or choices.dim() != 3:
+        raise ValueError("choices must be a [K, T, top] tensor")
+    k, t, e = shape = logits.shape
+    xl, xt = _view(logits, "logits", _FLOAT_TYPES, shape)
+    cl, ct = _view(choices, "choices", _CHOICE_TYPES, (k, t, choices.shape[2]))
+    ns, = _view(counts, "counts", (torch.int64,), (k, e))
+    ml = ts = gl = gt = 0
+    bufs = [("loss", loss, torch.float32, (k,)), ("workspace", workspace, torch.uint8, None)]
+    views = [("logits", logits), ("choices", choices), ("counts", counts)]
+    if mask is not None:
+        ml, = _view(mask, "mask", _MASK_TYPES, (k, t))
+        views.append(("mask", mask))
+    if totals is not None:
+        ts, = _view(totals, "totals", (torch.int64,), (k, e))
+        views.append(("totals", totals))
+    if grad_logits is not None:
+        gl, gt = _view(grad_logits, "grad_logits", (logits.dtype,), shape)
+        views.append(("grad_logits", grad_logits))
+    if mean_probs is not None:
+        bufs.append(("mean_probs", mean_probs, torch.float32, (k, e)))
+    if grad_scale is not None:
+        bufs.append(("grad_scale", grad_scale, torch.float64, (k,)))
+    pres = _presence(present, k)
+    _check_views(bufs, views)
+    _on_device(logits.get_device(), stream, _lib.dlc_expert_balance, logits.data_ptr(), _FLOAT_TYPES[logits.dtype], xl,
+               xt, choices.data_ptr(), _CHOICE_TYPES[choices.dtype], cl, ct, _address(mask), ml, k, pres, t, e,
+               choices.shape[2], float(coef), loss.data_ptr(), counts.data_ptr(), ns, _address(mean_probs),
+               _address(totals), ts, _address(grad_logits), gl, gt, _address(grad_scale),
+               DLC_ACCUMULATE if accumulate else 0, workspace.data_ptr(), workspace.numel())
+
+
+def _check_views(bufs, views):
+    """Whole buffers as (name, tensor, dtype, shape or None) and views that are checked already:
+    all on one GPU."""
+    c = _Checks()
+    for name, t, dtype, shape in bufs:
+        c.need(t, name, dtype)
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    c.bufs.extend(views)
+    c.done()
+
+
+def _doubles(values, k: int, name: str) -> array.array:
+    if len(values) != k:
+        raise ValueError(f"{name} holds {len(values)} values for {k} learners")
+    return array.array("d", values)
+
+
+def dlc_expert_weights(counts, weights, expert_of, tensor_weights, token_weight=None, stream=None):
+    """Merge weights of every (tensor, learner), device fp64 [T, K], from the experts' counts, device
+    int64 [K, experts]: a tensor of expert expert_of[t] by the tokens that each present learner
+    (weights[i] > 0) sent to it, times token_weight[i] (default 1); a tensor of no expert
+    (-1), or of one that got no token, by `weights`.  expert_of: ints, or group_ids of them."""
+    if not isinstance(counts, torch.Tensor) or counts.dim() != 2:
+        raise ValueError("counts must be a [K, experts] tensor")
+    k, e = counts.shape
+    stride, = _view(counts, "counts", (torch.int64,), (k, e))
+    ids = group_ids(expert_of)
+    if ids is expert_of:  # the library reads it while other threads run: not the caller's own array
+        ids = ids[:]
+    w = _doubles(weights, k, "weights")
+    q = None if token_weight is None else _doubles(token_weight, k, "token_weight")
+    _check_views((("tensor_weights", tensor_weights, torch.float64, (len(ids), k)),), (("counts", counts),))
+    _on_device(counts.get_device(), stream, _lib.dlc_expert_weights, counts.data_ptr(), stride, k, e, _items(w),
+               _items(q), _items(ids), len(ids), tensor_weights.data_ptr())
+
+
+def dlc_outer_grad_norm_workspace_bytes(tensors) -> int:
+    arr, n = _tensors(tensors)
+    out = ctypes.c_size_t(0)
+    _check(_lib.dlc_outer_grad_norm_workspace_bytes(arr, n, ctypes.byref(out)))
+    return out.value
+
+
+def alloc_outer_grad_norm_workspace(tensors, device="cuda") -> torch.Tensor:
+    nbytes = max(256, dlc_outer_grad_norm_workspace_bytes(tensors))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _outer(codes, codebook, weights, tensors, tensor_weights, bufs):
+    """Checks that the merged gradient's calls share -> (K, learner_stride, weights as a C array)."""
+    k, stride = _row_shape(codes, tensors, "codes")
+    w = _doubles(weights, k, "weights")
+    nt = len(tensors)
+    if not isinstance(codebook, torch.Tensor):
+        raise TypeError(f"codebook must be a torch.Tensor, not {type(codebook).__name__}")
+    bufs = [("codes", codes, torch.uint8, (k, stride)), ("codebook", codebook, torch.float32, codebook.shape), *bufs]
+    if tensor_weights is not None:
+        bufs.append(("tensor_weights", tensor_weights, torch.float64, (nt, k)))
+    _check_buffers(bufs)
+    if codebook.numel() < k * nt * DLC_N_BUCKETS:
+        raise ValueError(f"codebook holds {codebook.numel()} elements; the call needs at least {k * nt * DLC_N_BUCKETS}")
+    return k, stride, w
+
+
+def dlc_outer_grad_norm(codes, codebook, weights, tensors, norm, grad_scale, workspace, max_norm=float("inf"),
+                        tensor_weights=None, stream=None):
+    """The merged outer gradient's norm over all tensors into norm, and the factor that clips it to
+    max_norm into grad_scale (0 where the norm is not finite); both device fp64 [1].
+    tensor_weights: device fp64 [T, K] (dlc_expert_weights) in place of the normalized weights."""
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError(f"workspace must be a torch.Tensor, not {type(workspace).__name__}")
+    k, stride, w = _outer(codes, codebook, weights, tensors, tensor_weights,
+                          (("norm", norm, torch.float64, (1,)), ("grad_scale", grad_scale, torch.float64, (1,)),
+                           ("workspace", workspace, torch.uint8, workspace.shape)))
+    arr, n = _tensors(tensors)
+    _on_device(codes.get_device(), stream, _lib.dlc_outer_grad_norm, codes.data_ptr(), stride, k, codebook.data_ptr(),
+               _items(w), _address(tensor_weights), arr, n, float(max_norm), norm.data_ptr(), grad_scale.data_ptr(),
+               workspace.data_ptr(), workspace.numel())
+
+
+def dlc_merge_clipped_step(theta_g, momentum, codes, codebook, weights, tensors, grad_scale=None, tensor_weights=None,
+                           lr=0.7, beta=0.9, stream=None):
+    """dlc_merge_outer_step with the merged gradient times grad_scale (device fp64 [1]; the step is
+    left out unless it is finite and positive) and, with tensor_weights, each tensor's own
+    weights."""
+    end, _ = _extents(tensors)
+    bufs = []
+    for name, t in (("theta_g", theta_g), ("momentum", momentum)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
+        if t.numel() < end:
+            raise ValueError(f"{name} holds {t.numel()} elements; the call needs at least {end}")
+        bufs.append((name, t, torch.float32, t.shape))
+    if grad_scale is not None:
+        bufs.append(("grad_scale", grad_scale, torch.float64, (1,)))
+    k, stride, w = _outer(codes, codebook, weights, tensors, tensor_weights, bufs)
+    arr, n = _tensors(tensors)
+    _on_device(codes.get_device(), stream, _lib.dlc_merge_clipped_step, theta_g.data_ptr(), momentum.data_ptr(),
+               codes.data_ptr(), stride, k, codebook.data_ptr(), _items(w), _address(tensor_weights),
+               _address(grad_scale), arr, n, float(lr), float(beta))

@@ -50,6 +50,18 @@ int32_t hip_fail(hipError_t e, const char* what) {
   return fail(DLC_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
 }
 
+int32_t check_stretches(const Stretch* s, int32_t n) {
+  for (int32_t a = 0; a < n; ++a) {
+    for (int32_t b = 0; b < a; ++b) {
+      if (!(s[a].written || s[b].written) || !s[a].p || !s[b].p || s[a].bytes == 0 || s[b].bytes == 0) continue;
+      const uintptr_t x = reinterpret_cast<uintptr_t>(s[a].p), y = reinterpret_cast<uintptr_t>(s[b].p);
+      if (x < y + s[b].bytes && y < x + s[a].bytes)
+        return fail(DLC_ERR_INVALID_ARGUMENT, "the call's buffers must not overlap");
+    }
+  }
+  return DLC_OK;
+}
+
 int32_t check_tensors(const dlc_tensor* t, int32_t n, int64_t learner_stride, bool need_loffset) {
   if (t == nullptr) return fail(DLC_ERR_INVALID_ARGUMENT, "tensors is NULL");
   if (n < 1) return fail(DLC_ERR_INVALID_ARGUMENT, "n_tensors must be >= 1");
@@ -89,9 +101,11 @@ int32_t check_tensors(const dlc_tensor* t, int32_t n, int64_t learner_stride, bo
 }  // namespace dlc
 
 using dlc::aligned256;
+using dlc::aligned8;
 using dlc::check_tensors;
 using dlc::fail;
 using dlc::hip_fail;
+using dlc::no_throw;
 using dlc::ok;
 using dlc::round256;
 
@@ -298,17 +312,8 @@ int32_t run_encode(Common& c) {
   return DLC_OK;
 }
 
-// Merge arguments: checks and fp64 weight normalization (left-to-right sum).
-int32_t prepare_merge(dlc::MergeArgs& a, float* theta_global, float* momentum, const uint8_t* codes,
-                      int64_t learner_stride, int32_t n_learners, const float* codebook, const double* weights,
-                      double lr, double beta) {
-  if (n_learners < 1 || n_learners > DLC_MAX_LEARNERS)
-    return fail(DLC_ERR_INVALID_ARGUMENT, "n_learners must be in [1, 64]");
-  if (!theta_global || !momentum || !codes || !codebook || !weights)
-    return fail(DLC_ERR_INVALID_ARGUMENT, "theta_global, momentum, codes, codebook and weights must not be NULL");
-  if (!aligned256(theta_global) || !aligned256(momentum) || !aligned256(codes) || !aligned256(codebook))
-    return fail(DLC_ERR_ALIGNMENT, "device pointers must be 256-byte aligned");
-  if (!std::isfinite(lr) || !std::isfinite(beta)) return fail(DLC_ERR_INVALID_ARGUMENT, "lr and beta must be finite");
+// The present learners and their weights, normalized in fp64 (left-to-right sum).
+int32_t merge_weights(dlc::MergeArgs& a, const double* weights, int32_t n_learners) {
   double total = 0.0;
   for (int32_t i = 0; i < n_learners; ++i) {
     if (!(weights[i] >= 0.0) || !std::isfinite(weights[i]))
@@ -325,12 +330,29 @@ int32_t prepare_merge(dlc::MergeArgs& a, float* theta_global, float* momentum, c
       ++kp;
     }
   }
+  a.n_present = kp;
+  a.n_learners = n_learners;
+  return DLC_OK;
+}
+
+// Merge arguments: checks and weights.
+int32_t prepare_merge(dlc::MergeArgs& a, float* theta_global, float* momentum, const uint8_t* codes,
+                      int64_t learner_stride, int32_t n_learners, const float* codebook, const double* weights,
+                      double lr, double beta) {
+  if (n_learners < 1 || n_learners > DLC_MAX_LEARNERS)
+    return fail(DLC_ERR_INVALID_ARGUMENT, "n_learners must be in [1, 64]");
+  if (!theta_global || !momentum || !codes || !codebook || !weights)
+    return fail(DLC_ERR_INVALID_ARGUMENT, "theta_global, momentum, codes, codebook and weights must not be NULL");
+  if (!aligned256(theta_global) || !aligned256(momentum) || !aligned256(codes) || !aligned256(codebook))
+    return fail(DLC_ERR_ALIGNMENT, "device pointers must be 256-byte aligned");
+  if (!std::isfinite(lr) || !std::isfinite(beta)) return fail(DLC_ERR_INVALID_ARGUMENT, "lr and beta must be finite");
+  const int32_t rc = merge_weights(a, weights, n_learners);
+  if (rc != DLC_OK) return rc;
   a.theta_g = theta_global;
   a.momentum = momentum;
   a.codes = codes;
   a.codebook = codebook;
   a.stride = learner_stride;
-  a.n_present = kp;
   a.lr = lr;
   a.beta = beta;
   return DLC_OK;
@@ -346,6 +368,23 @@ int32_t run_merge(const dlc::MergeArgs& a, const dlc_tensor* tensors, int32_t n_
   }
   return DLC_OK;
 }
+
+// What a merge reads: the codes from the first learner's first tensor to the last
+// learner's last one, the codebooks, the weights.
+struct OuterInputs {
+  dlc::Stretch codes, codebook, weights;
+  OuterInputs(const uint8_t* c, int64_t stride, int32_t n_learners, const float* cb, const double* tensor_weights,
+              const dlc_tensor* t, int32_t n) {
+    int64_t first = t[0].loffset, last = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      first = std::min(first, t[i].loffset);
+      last = std::max(last, t[i].loffset + t[i].numel);
+    }
+    codes = {c + first, (uint64_t)(n_learners - 1) * stride + (uint64_t)(last - first), false};
+    codebook = {cb, (uint64_t)n_learners * n * DLC_N_BUCKETS * sizeof(float), false};
+    weights = {tensor_weights, (uint64_t)n_learners * n * sizeof(double), false};
+  }
+};
 
 int32_t run_broadcast(const float* theta_global, float* theta_learners, int64_t learner_stride, int32_t n_learners,
                       const uint8_t* rows, const dlc_tensor* tensors, int32_t n_tensors, hipStream_t s) {
@@ -1204,6 +1243,89 @@ int32_t dlc_rda_outer_step(float* theta_global, float* momentum, const float* th
   ma.dir_part = nullptr;
   rc = run_merge(ma, tensors, n_tensors, 0, -1, st);
   return rc == DLC_OK ? ok() : rc;
+}
+
+int32_t dlc_outer_grad_norm_workspace_bytes(const dlc_tensor* tensors, int32_t n_tensors, size_t* bytes) {
+  return no_throw([&]() -> int32_t {
+    if (!bytes) return fail(DLC_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    const int32_t rc = check_tensors(tensors, n_tensors, 0, false);
+    if (rc != DLC_OK) return rc;
+    *bytes = round256((size_t)direction_partition(tensors, n_tensors).n_slots * sizeof(double));
+    return ok();
+  });
+}
+
+int32_t dlc_outer_grad_norm(const uint8_t* codes, int64_t learner_stride, int32_t n_learners, const float* codebook,
+                            const double* weights, const double* tensor_weights, const dlc_tensor* tensors,
+                            int32_t n_tensors, double max_norm, double* norm, double* grad_scale, void* workspace,
+                            size_t workspace_bytes, void* hip_stream) {
+  return no_throw([&]() -> int32_t {
+    if (n_learners < 1 || n_learners > DLC_MAX_LEARNERS)
+      return fail(DLC_ERR_INVALID_ARGUMENT, "n_learners must be in [1, 64]");
+    if (!codes || !codebook || !weights || !norm || !grad_scale)
+      return fail(DLC_ERR_INVALID_ARGUMENT, "codes, codebook, weights, norm and grad_scale must not be NULL");
+    if (!aligned256(codes) || !aligned256(codebook))
+      return fail(DLC_ERR_ALIGNMENT, "device pointers must be 256-byte aligned");
+    if (!aligned8(tensor_weights) || !aligned8(norm) || !aligned8(grad_scale))
+      return fail(DLC_ERR_ALIGNMENT, "tensor_weights, norm and grad_scale must be 8-byte aligned");
+    if (!(max_norm > 0.0)) return fail(DLC_ERR_INVALID_ARGUMENT, "max_norm must be > 0");
+    dlc::MergeArgs a;
+    int32_t rc = merge_weights(a, weights, n_learners);
+    if (rc == DLC_OK) rc = check_tensors(tensors, n_tensors, learner_stride, true);
+    if (rc != DLC_OK) return rc;
+    const Partition p = direction_partition(tensors, n_tensors);
+    const size_t need = round256((size_t)p.n_slots * sizeof(double));
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(DLC_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
+    if (!aligned256(workspace)) return fail(DLC_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+    const OuterInputs in(codes, learner_stride, n_learners, codebook, tensor_weights, tensors, n_tensors);
+    const dlc::Stretch s[] = {in.codes, in.codebook, in.weights, {norm, sizeof(double), true},
+                              {grad_scale, sizeof(double), true}, {workspace, need, true}};
+    rc = dlc::check_stretches(s, (int32_t)(sizeof(s) / sizeof(s[0])));
+    if (rc != DLC_OK) return rc;
+    a.codes = codes;
+    a.codebook = codebook;
+    a.stride = learner_stride;
+    a.tensor_w = tensor_weights;
+    a.dir_part = static_cast<double*>(workspace);
+    const hipStream_t st = static_cast<hipStream_t>(hip_stream);
+    for (const dlc::LaunchGeom& g : p.launches) {
+      const hipError_t e = dlc::launch_outer_squares(a, g, st);
+      if (e != hipSuccess) return hip_fail(e, "outer gradient kernel launch");
+    }
+    const hipError_t e = dlc::launch_outer_norm({a.dir_part, norm, grad_scale, max_norm, p.n_slots}, st);
+    return e != hipSuccess ? hip_fail(e, "outer gradient norm kernel launch") : ok();
+  });
+}
+
+int32_t dlc_merge_clipped_step(float* theta_global, float* momentum, const uint8_t* codes, int64_t learner_stride,
+                               int32_t n_learners, const float* codebook, const double* weights,
+                               const double* tensor_weights, const double* grad_scale, const dlc_tensor* tensors,
+                               int32_t n_tensors, double lr, double beta, void* hip_stream) {
+  return no_throw([&]() -> int32_t {
+    dlc::MergeArgs a;
+    int32_t rc = prepare_merge(a, theta_global, momentum, codes, learner_stride, n_learners, codebook, weights, lr, beta);
+    if (rc != DLC_OK) return rc;
+    if (!aligned8(tensor_weights) || !aligned8(grad_scale))
+      return fail(DLC_ERR_ALIGNMENT, "tensor_weights and grad_scale must be 8-byte aligned");
+    rc = check_tensors(tensors, n_tensors, learner_stride, true);
+    if (rc != DLC_OK) return rc;
+    int64_t first = tensors[0].offset, last = 0;
+    for (int32_t t = 0; t < n_tensors; ++t) {
+      first = std::min(first, tensors[t].offset);
+      last = std::max(last, tensors[t].offset + tensors[t].numel);
+    }
+    const OuterInputs in(codes, learner_stride, n_learners, codebook, tensor_weights, tensors, n_tensors);
+    const uint64_t span = (uint64_t)(last - first) * sizeof(float);
+    const dlc::Stretch s[] = {in.codes, in.codebook, in.weights, {grad_scale, sizeof(double), false},
+                              {theta_global + first, span, true}, {momentum + first, span, true}};
+    rc = dlc::check_stretches(s, (int32_t)(sizeof(s) / sizeof(s[0])));
+    if (rc != DLC_OK) return rc;
+    a.tensor_w = tensor_weights;
+    a.scale = grad_scale;
+    rc = run_merge(a, tensors, n_tensors, 0, -1, static_cast<hipStream_t>(hip_stream));
+    return rc == DLC_OK ? ok() : rc;
+  });
 }
 
 const char* dlc_last_error(void) { return dlc::last_error(); }

@@ -1,0 +1,77 @@
+// Launch descriptors of the mixture-of-experts calls (the router's balance loss, merge
+// weights from expert counts), shared by the host orchestration and the gfx950 kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "dlc_inner.h"
+
+namespace dlc {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxChoices = 64;
+constexpr int kBalanceBlock = 512;       // threads of a block over the logits
+constexpr int kBalanceOne = 1024;        // threads of the block that does a learner's whole call
+constexpr int kCountBlock = 512;
+constexpr int kFoldTokens = 16;          // tokens a lane sums in fp32 before it goes on in fp64
+constexpr int kCountWords = 4096;        // LDS words of a block's histogram copies
+constexpr int64_t kCountTokens = 1 << 18;  // most tokens of a counting block, see divide()
+
+struct BalanceArgs {
+  const void* logits;         // [n_learners][tokens][experts], strides in elements
+  int64_t x_learner, x_token;
+  const void* choices;        // [n_learners][tokens][top]
+  int64_t c_learner, c_token;
+  const uint8_t* mask;        // [n_learners][tokens], or NULL
+  int64_t mask_learner;
+  void* grad;                 // [n_learners][tokens][experts], or NULL
+  int64_t g_learner, g_token;
+  const double* grad_scale;   // [n_learners], or NULL
+  float* loss;                // [n_learners]
+  int64_t* counts;            // [n_learners][experts]
+  int64_t counts_stride;
+  float* means;               // [n_learners][experts], or NULL
+  int64_t* totals;            // [n_learners][experts], or NULL
+  int64_t totals_stride;
+  uint32_t* part_counts;      // [present][count_blocks][experts + 1]: counts, kept tokens
+  double* part_probs;         // [present][blocks][experts] sums of probabilities
+  double coef;
+  int32_t tokens, experts, top;
+  uint32_t top_inverse;       // ceil(2^32 / top), 0 for top = 1
+  int32_t count_blocks, count_tokens;  // blocks per learner that count, tokens of each
+  int32_t blocks, block_tokens;        // blocks per learner over the logits, tokens of each
+  int32_t accumulate, wide_choices;
+  int32_t n_present;
+  LearnerList learner;
+};
+
+constexpr int kWeightTensors = 640;      // tensors per launch
+
+struct WeightArgs {
+  const int64_t* counts;
+  int64_t counts_stride;
+  double* out;                // [n_tensors][n_learners]
+  int32_t n_learners;
+  int32_t n_tensors;          // of this launch
+  int64_t first;              // its first tensor
+  double w_hat[64];           // normalized weights, 0 = absent
+  double token_weight[64];    // 0 for absent learners
+  int16_t expert[kWeightTensors];
+};
+
+static_assert(sizeof(BalanceArgs) <= 4096 && sizeof(WeightArgs) <= 4096);
+
+// Kernel launchers (dlc_experts.hip).  Each returns hipSuccess or the launch error.
+// one kernel, a block per learner
+hipError_t launch_balance_one(const BalanceArgs& a, int32_t type, hipStream_t s);
+hipError_t launch_balance_count(const BalanceArgs& a, hipStream_t s);
+// with a gradient after launch_balance_count; without one it counts its own tokens' choices
+hipError_t launch_balance(const BalanceArgs& a, int32_t type, hipStream_t s);
+hipError_t launch_balance_final(const BalanceArgs& a, hipStream_t s);
+// tokens that a block of `threads` threads takes at once
+int32_t balance_tokens(int32_t type, int32_t experts, int32_t threads);
+hipError_t launch_expert_weights(const WeightArgs& a, hipStream_t s);
+
+}  // namespace dlc

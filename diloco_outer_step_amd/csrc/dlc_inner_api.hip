@@ -15,10 +15,12 @@
 namespace {
 
 using dlc::aligned256;
+using dlc::aligned8;
 using dlc::check_tensors;
 using dlc::fail;
 using dlc::hip_fail;
 using dlc::kMaxTensorNumel;
+using dlc::no_throw;
 using dlc::ok;
 using dlc::round256;
 
@@ -130,8 +132,6 @@ bool small_norm(const std::vector<Range>& ranges) {
 // for a call of 9100 blocks that takes 31.
 constexpr int64_t kMaxTickets = 64;
 
-bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
-
 // The present learners' indices -> list (zeroed before), their number; *rc is the status.
 int32_t present_learners(int32_t n_learners, const uint8_t* present, dlc::LearnerList& list, int32_t* rc) {
   *rc = DLC_OK;
@@ -211,16 +211,6 @@ int32_t check_float_type(int32_t type, const char* name, bool wide) {
 }
 
 int32_t element_bytes(int32_t type) { return type == DLC_FLOAT32 ? 4 : 2; }
-
-// No C++ exception crosses the ABI: running out of host memory is an error code.
-template <typename F>
-int32_t no_throw(F&& f) noexcept {
-  try {
-    return f();
-  } catch (...) {
-    return dlc::out_of_memory();
-  }
-}
 
 // The moments of an AdamW call: 32-bit, or codes and scale bytes.
 struct Moments {

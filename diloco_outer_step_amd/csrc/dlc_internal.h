@@ -103,6 +103,18 @@ struct MergeArgs {
   const double* norm2;      // [n_learners][rows] squared norms of the dequantized pseudo-gradients
   double* dir_part;         // [slot] per-block sums of the squared averaged direction
   double* coef;             // [row][n_present] coefficient of each learner's codebook in g
+  // The clipped step and the merged gradient's norm (null elsewhere):
+  const double* tensor_w;   // [row][n_learners] weights in place of w_hat
+  int32_t n_learners;       // row length of tensor_w
+  const double* scale;      // factor of g; the step is left out unless it is finite and positive
+};
+
+struct OuterNormArgs {
+  const double* part;       // [n_slots] sums of squares
+  double* norm;
+  double* grad_scale;
+  double max_norm;
+  int64_t n_slots;
 };
 
 struct BroadcastArgs {
@@ -143,6 +155,9 @@ hipError_t launch_merge(const MergeArgs& a, const LaunchGeom& g, hipStream_t s);
 // block, then each tensor's learner coefficients (which k_merge then uses)
 hipError_t launch_rda_direction(const MergeArgs& a, const LaunchGeom& g, hipStream_t s);
 hipError_t launch_rda_coef(const MergeArgs& a, const LaunchGeom& g, hipStream_t s);
+// The merged gradient's norm: sums of squares per block (dir_part), then norm and factor
+hipError_t launch_outer_squares(const MergeArgs& a, const LaunchGeom& g, hipStream_t s);
+hipError_t launch_outer_norm(const OuterNormArgs& a, hipStream_t s);
 hipError_t launch_broadcast(const BroadcastArgs& a, const LaunchGeom& g, hipStream_t s);
 // segments: (offset of the chunk in theta_g, the receiver's offset in the flat theta_L / accum,
 // numel); the sender's codes sit one rank row earlier, cyclically; the launch geometry must be the

@@ -865,6 +865,13 @@ __device__ __forceinline__ double rda_unit_weight(const MergeArgs& a, const Laun
   return n2 > 0.0 ? a.w_hat[k] / __builtin_sqrt(n2) : 0.0;
 }
 
+//
+// The clipped step's table holds scale * w * codebook_i[c] with the tensor's own weights
+// w, and DIR without norm2 sums the squares of the merged gradient with them.
+__device__ __forceinline__ double merge_weight(const MergeArgs& a, size_t trow, int k) {
+  return a.tensor_w != nullptr ? a.tensor_w[trow * a.n_learners + a.learner[k]] : a.w_hat[k];
+}
+
 template <int NR, bool DIR = false>
 __global__ __launch_bounds__(kMergeBlock) __attribute__((amdgpu_waves_per_eu(4))) void k_merge(
     const MergeArgs a, const LaunchGeom g) {
@@ -877,14 +884,16 @@ __global__ __launch_bounds__(kMergeBlock) __attribute__((amdgpu_waves_per_eu(4))
   const Span sp = block_span(g);
   const TensorDesc td = g.t[sp.t];
   const size_t trow = (size_t)g.row_base + g.t_base + sp.t;
+  const double scale = !DIR && a.scale != nullptr ? *a.scale : 1.0;
+  if (!(scale > 0.0 && __builtin_isfinite(scale))) return;
 
   for (int i = threadIdx.x; i < kp * kBuckets; i += kMergeBlock) {
     const int k = i >> 8, c = i & (kBuckets - 1);
     const float cb = a.codebook[((size_t)a.learner[k] * g.n_tensors_call + trow) * kBuckets + c];
     double w;
-    if (DIR) w = rda_unit_weight(a, g, trow, k);
-    else w = a.coef != nullptr ? a.coef[trow * kp + k] : a.w_hat[k];
-    tab[i] = w * (double)cb;
+    if (DIR) w = a.norm2 != nullptr ? rda_unit_weight(a, g, trow, k) : merge_weight(a, trow, k);
+    else w = a.coef != nullptr ? a.coef[trow * kp + k] : scale * merge_weight(a, trow, k);
+    tab[i] = w != 0.0 ? w * (double)cb : 0.0;  // a weight of 0 leaves the learner out, whatever its codebook holds
   }
   __syncthreads();
   double dsum = 0.0;  // DIR: this thread's sum of squared direction values
@@ -1043,6 +1052,25 @@ __global__ __launch_bounds__(kBuckets) void k_rda_coef(const MergeArgs a, const 
   }
   __syncthreads();
   for (int k = threadIdx.x; k < kp; k += kBuckets) a.coef[trow * kp + k] = scale * rda_unit_weight(a, g, trow, k);
+}
+
+// k_outer_norm: the blocks' sums of squares in a fixed order -> norm and clipping factor.
+constexpr int kOuterNormThreads = 1024;
+
+__global__ __launch_bounds__(kOuterNormThreads) void k_outer_norm(const OuterNormArgs a) {
+  __shared__ double red[kOuterNormThreads / 64];
+  double v = 0.0;
+  for (int64_t b = threadIdx.x; b < a.n_slots; b += kOuterNormThreads) v += a.part[b];
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double sum = 0.0;
+    for (int i = 0; i < kOuterNormThreads / 64; ++i) sum += red[i];
+    const double n = __builtin_sqrt(sum);
+    *a.norm = n;
+    *a.grad_scale = !__builtin_isfinite(n) ? 0.0 : n > a.max_norm ? a.max_norm / n : 1.0;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1359,6 +1387,15 @@ hipError_t launch_rda_direction(const MergeArgs& a, const LaunchGeom& g, hipStre
     case 8: return launch_rda_direction_r<8>(a, g, s);
     default: return launch_rda_direction_r<0>(a, g, s);
   }
+}
+
+hipError_t launch_outer_squares(const MergeArgs& a, const LaunchGeom& g, hipStream_t s) {
+  return launch_rda_direction(a, g, s);
+}
+
+hipError_t launch_outer_norm(const OuterNormArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(k_outer_norm, dim3(1), dim3(kOuterNormThreads), 0, s, a);
+  return hipGetLastError();
 }
 
 hipError_t launch_rda_coef(const MergeArgs& a, const LaunchGeom& g, hipStream_t s) {

@@ -93,6 +93,15 @@ extern "C" {
 /* Consecutive elements that share a scale byte in dlc_adamw_coded_step. */
 #define DLC_CODE_BLOCK 64
 
+/* dlc_expert_balance: experts of a router, choices per token, tokens per learner; types
+   of the choices; flag: add to grad_logits instead of writing it. */
+#define DLC_MAX_EXPERTS 1024
+#define DLC_MAX_CHOICES 64
+#define DLC_MAX_TOKENS 16777216
+#define DLC_INT32 0
+#define DLC_INT64 1
+#define DLC_ACCUMULATE 16u
+
 typedef struct dlc_tensor {
     int64_t offset;   /* element offset into theta_global and momentum        */
     int64_t loffset;  /* element offset into each learner row (theta, codes)  */
@@ -583,6 +592,139 @@ int32_t dlc_adamw_coded_step(float* theta_learners, const void* grads, int32_t g
                              const dlc_adamw_group* groups, int32_t n_groups, uint64_t seed,
                              const double* grad_scale, const double* lr_scale, void* working, int32_t working_type,
                              void* hip_stream);
+
+/*
+ * Mixtures of experts under the outer step.  A learner's router sends every token to a
+ * few of the experts.  dlc_expert_balance is the router's auxiliary loss in the inner
+ * step, and counts what each expert received; dlc_expert_weights turns those counts into
+ * merge weights, so that a tensor that belongs to one expert is merged by the tokens
+ * that this expert saw in each learner (Decoupled DiLoCo digest, "fault tolerance" item
+ * 3: learners that processed more tokens weigh more); dlc_outer_grad_norm and
+ * dlc_merge_clipped_step merge with them, and clip the outer gradient to a global norm.
+ * The pages give no formulas; the usual ones are taken.  Every call can be captured in
+ * a HIP graph and replayed; none synchronizes or keeps anything between calls.
+ */
+
+/*
+ * dlc_expert_balance -- per-expert counts, the balance loss and its gradient, for every
+ * present learner in one call.  With x[t][e] the router's logits, the tokens t that the
+ * mask keeps (n of them), p[t] = softmax(x[t]) and top choices per token:
+ *   counts[e]     = number of choices of expert e among the kept tokens
+ *   mean_probs[e] = sum_t p[t][e] / n
+ *   loss          = coef * E * sum_e counts[e] / (n top) * mean_probs[e]
+ *                   (coef for an even router, up to coef E for one that uses one expert)
+ *   grad_logits[t][e] = grad_scale * d loss / d x[t][e]
+ *                 = grad_scale * coef * E / (n^2 top) * p[t][e] * (c[e] - sum_j p[t][j] c[j]),
+ *                   c = counts less their mean; 0 where the mask leaves a token out
+ *   totals[e]    += counts[e]
+ * The counts are constants in the gradient, as a choice has none.  A learner with no kept
+ * token has counts, mean_probs and loss 0.  A choice outside [0, E) is one that was
+ * dropped: it counts for no expert.  A logit of -infinity has probability 0; a token
+ * whose logits are all -infinity has no probabilities and a zero gradient.  Logits of NaN
+ * or +infinity make their token's gradient, the mean probabilities and the loss NaN.
+ * What the mask leaves out has no influence, whatever it holds.
+ *   logits        device, of logits_type (DLC_FLOAT32, DLC_BFLOAT16, DLC_FLOAT16): element
+ *                 (i, t, e) at i * logits_learner_stride + t * logits_token_stride + e
+ *                 elements; strides >= 0, aligned to its elements
+ *   choices       device, of choices_type (DLC_INT32, DLC_INT64), element (i, t, j) with its
+ *                 own two strides likewise
+ *   mask          device uint8, (i, t) at i * mask_learner_stride + t: 0 leaves the token
+ *                 out; NULL = all kept
+ *   present       host uint8 [n_learners] (0 = absent: nothing of it is read or written) or
+ *                 NULL = all present; at least one present (else DLC_ERR_NO_QUORUM)
+ *   n_tokens      0..DLC_MAX_TOKENS per learner (with 0, logits and choices may be NULL)
+ *   n_experts     1..DLC_MAX_EXPERTS;  n_choices 1..min(n_experts, DLC_MAX_CHOICES)
+ *   coef          finite
+ *   loss          device fp32 [n_learners]
+ *   counts        device int64, (i, e) at i * counts_stride + e
+ *   mean_probs    device fp32 [n_learners][n_experts], or NULL
+ *   totals        device int64, (i, e) at i * totals_stride + e, or NULL: tokens of each
+ *                 expert since the last outer step, as dlc_expert_weights takes them
+ *                 (several layers' experts side by side in a row, each layer with its own call)
+ *   grad_logits   device, of logits_type, with its own two strides (the rows may not overlap);
+ *                 NULL = no gradient, and the logits are then read without waiting for the counts
+ *   grad_scale    device fp64 [n_learners], or NULL = 1: the loss scale or the upstream gradient
+ *   flags         0, or DLC_ACCUMULATE: grad_logits += (one rounding; tokens that are left
+ *                 out keep their values)
+ *   workspace     >= dlc_expert_balance_workspace_bytes(n_learners, n_tokens, n_experts)
+ *                 bytes, 256-byte aligned, no initial contents required
+ * The probabilities are fp32 (each within 2^-17 of itself for logits within 16 of the row's
+ * largest), summed in fp32 over at most 16 tokens and from there on in fp64 in a fixed
+ * order: repeated calls agree bit for bit.  No written buffer may overlap another, each
+ * taken from its first to its last element: DLC_ERR_INVALID_ARGUMENT.
+ */
+int32_t dlc_expert_balance_workspace_bytes(int32_t n_learners, int64_t n_tokens, int32_t n_experts, size_t* bytes);
+
+int32_t dlc_expert_balance(const void* logits, int32_t logits_type, int64_t logits_learner_stride,
+                           int64_t logits_token_stride, const void* choices, int32_t choices_type,
+                           int64_t choices_learner_stride, int64_t choices_token_stride, const uint8_t* mask,
+                           int64_t mask_learner_stride, int32_t n_learners, const uint8_t* present, int64_t n_tokens,
+                           int32_t n_experts, int32_t n_choices, double coef, float* loss, int64_t* counts,
+                           int64_t counts_stride, float* mean_probs, int64_t* totals, int64_t totals_stride,
+                           void* grad_logits, int64_t grad_learner_stride, int64_t grad_token_stride,
+                           const double* grad_scale, uint32_t flags, void* workspace, size_t workspace_bytes,
+                           void* hip_stream);
+
+/*
+ * dlc_expert_weights -- merge weights of every (tensor, learner) from the experts'
+ * counts.  For tensor t of expert e = expert_of[t]:
+ *   tensor_weights[t][i] = r_i / sum_j r_j, r_i = token_weight[i] * counts[i][e]  (fp64,
+ *                          left-to-right sum, over the learners with weights[i] > 0)
+ * and for a tensor of no expert (-1), or of an expert to which no present learner sent a
+ * token, weights[i] / sum_j weights[j], as dlc_merge_outer_step weighs it.  Absent learners'
+ * entries (weights[i] = 0) are 0, and their counts are not read.
+ *   counts         device int64 >= 0 (a negative one counts as 0), (i, e) at
+ *                  i * counts_stride + e, read only
+ *   weights        host double [n_learners], as dlc_merge_outer_step's
+ *   token_weight   host double [n_learners], finite and >= 0, or NULL = 1: what a learner's
+ *                  token is worth (a discount for stale learners)
+ *   expert_of      host int32 [n_tensors], each -1 or in [0, n_experts)
+ *   tensor_weights device fp64 [n_tensors][n_learners], written
+ */
+int32_t dlc_expert_weights(const int64_t* counts, int64_t counts_stride, int32_t n_learners, int32_t n_experts,
+                           const double* weights, const double* token_weight, const int32_t* expert_of,
+                           int32_t n_tensors, double* tensor_weights, void* hip_stream);
+
+/*
+ * dlc_outer_grad_norm -- the global norm of the merged outer gradient over all tensors of
+ * the call, and the factor that clips it.  With g as in dlc_merge_outer_step:
+ *   norm[0]       = sqrt(sum of g^2)                     (fp64, in a fixed order)
+ *   grad_scale[0] = min(1, max_norm / norm), or 0 where norm is not finite
+ *                   (dlc_merge_clipped_step then leaves the step out)
+ *   codes, codebook, weights  as dlc_merge_outer_step
+ *   tensor_weights  device fp64 [n_tensors][n_learners] (dlc_expert_weights): tensor t
+ *                   takes tensor_weights[t][i] in place of w_hat_i, for learners with
+ *                   weights[i] > 0; finite, 0 = this learner has no part in this tensor;
+ *                   NULL = w_hat_i everywhere
+ *   max_norm        > 0; INFINITY = no clipping
+ *   norm, grad_scale  device fp64 [1], written
+ *   workspace       >= dlc_outer_grad_norm_workspace_bytes(tensors, n_tensors) bytes,
+ *                   256-byte aligned, no initial contents required
+ * No written buffer may overlap another.
+ */
+int32_t dlc_outer_grad_norm_workspace_bytes(const dlc_tensor* tensors, int32_t n_tensors, size_t* bytes);
+
+int32_t dlc_outer_grad_norm(const uint8_t* codes, int64_t learner_stride, int32_t n_learners, const float* codebook,
+                            const double* weights, const double* tensor_weights, const dlc_tensor* tensors,
+                            int32_t n_tensors, double max_norm, double* norm, double* grad_scale, void* workspace,
+                            size_t workspace_bytes, void* hip_stream);
+
+/*
+ * dlc_merge_clipped_step -- dlc_merge_outer_step with weights of its own for every tensor
+ * and with g scaled by a factor on the device:
+ *   g = sum_i (s * w_i) * codebook[i][t][code_i],  s = grad_scale[0],
+ *       w_i = tensor_weights[t][i], or w_hat_i without them
+ * (fp64).  A factor that is not finite and positive leaves the step out: nothing is
+ * written.  A factor from dlc_outer_grad_norm over a whole model serves each of its fragments.
+ *   grad_scale      device fp64 [1], or NULL = 1
+ *   tensor_weights  as dlc_outer_grad_norm
+ * Other arguments and errors as dlc_merge_outer_step, with which the call agrees bit for bit
+ * where both are NULL.  Neither theta_global nor momentum may overlap another buffer.
+ */
+int32_t dlc_merge_clipped_step(float* theta_global, float* momentum, const uint8_t* codes, int64_t learner_stride,
+                               int32_t n_learners, const float* codebook, const double* weights,
+                               const double* tensor_weights, const double* grad_scale, const dlc_tensor* tensors,
+                               int32_t n_tensors, double lr, double beta, void* hip_stream);
 
 /* Message of the last error on the calling thread ("" if none). */
 const char* dlc_last_error(void);
