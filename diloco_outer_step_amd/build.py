@@ -27,7 +27,8 @@ OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdlc.so")
 LIB_HOSTSAN = os.path.join(PKG, "libdlc_hostsan.so")
 API_SOURCES = ["dlc_api.hip", "dlc_inner_api.hip", "dlc_experts_api.hip"]  # host code only: sanitized in libdlc_hostsan.so
-SOURCES = [*API_SOURCES, "dlc_kernels.hip", "dlc_inner.hip", "dlc_experts.hip"]
+SOURCES = [*API_SOURCES, "dlc_kernels.hip", "dlc_inner.hip", "dlc_experts.hip",
+           "dlc_balance_f32.hip", "dlc_balance_bf16.hip", "dlc_balance_f16.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

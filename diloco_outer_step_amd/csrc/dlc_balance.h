@@ -1,0 +1,562 @@
+// The balance loss's kernels over the logits, compiled once for each type of them
+// (dlc_balance_*.hip).
+//
+//   k_balance      softmax of every token, its sum over the tokens, its gradient
+//   k_balance_one  a learner's whole call in one block, for few tokens
+//
+// The gradient of the loss coef E sum_e f_e P_e, f the share of the choices and P the mean
+// probabilities, is a softmax's: coef E / (n^2 top) p_e (c_e - sum_j p_j c_j).  It needs the
+// whole counts but not P, so the choices (a fiftieth of the logits' bytes) are counted first
+// and the logits are read once.  Taking c less its mean changes nothing, as sum p = 1, and
+// keeps the bracket from cancelling when the experts are used evenly.
+#pragma once
+
+#include "dlc_experts.h"
+
+#include <type_traits>
+
+namespace dlc {
+namespace {
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+// f of v and of the other half's value, for each group of L lanes whose halves hold one value
+// each.  Within rows of 16 lanes the other half is read by the instruction that uses it;
+// rows are exchanged by a swap of which both results are used.
+template <int L, typename F>
+__device__ __forceinline__ float with_other_half(float v, F&& f) {
+  const int x = __builtin_bit_cast(int, v);
+  int y = x, z = x;
+  if constexpr (L == 2) y = __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true);    // quad 1 0 3 2
+  if constexpr (L == 4) y = __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true);    // quad 2 3 0 1
+  if constexpr (L == 8) y = __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true);   // half row mirrored
+  if constexpr (L == 16) y = __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, true);  // row mirrored
+  if constexpr (L == 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    y = (int)r[0];
+    z = (int)r[1];
+  }
+  if constexpr (L == 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    y = (int)r[0];
+    z = (int)r[1];
+  }
+  return f(__builtin_bit_cast(float, z), __builtin_bit_cast(float, y));
+}
+
+template <int L, typename F>
+__device__ __forceinline__ float reduce(float v, F&& f) {
+  if constexpr (L >= 2) v = with_other_half<2>(v, f);
+  if constexpr (L >= 4) v = with_other_half<4>(v, f);
+  if constexpr (L >= 8) v = with_other_half<8>(v, f);
+  if constexpr (L >= 16) v = with_other_half<16>(v, f);
+  if constexpr (L >= 32) v = with_other_half<32>(v, f);
+  if constexpr (L >= 64) v = with_other_half<64>(v, f);
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// Counting
+// ---------------------------------------------------------------------------
+// f / top for f below kCountTokens top: the inverse is at most (top - 1) / 2^32 too large per
+// unit of f, and f (top - 1) < 2^18 64^2 <= 2^32.
+__device__ __forceinline__ uint32_t divide(uint32_t f, uint32_t inverse) {
+  return inverse == 0 ? f : __umulhi(f, inverse);
+}
+
+// A learner's choices of tokens [t0, t1) -> hist[0 .. experts), kept tokens -> hist[experts].
+// The words of hist hold copies of the histogram, so that lanes with the same choice (routers
+// have favourites, and few experts) add to different words: 16 at most, which are summed
+// at the end.
+template <int kThreads, typename I>
+__device__ __forceinline__ void count_choices(const BalanceArgs& a, int i, int t0, int t1, uint32_t* hist) {
+  const uint32_t e = (uint32_t)a.experts;
+  uint32_t copies = 1;
+  while (copies < 16 && copies * e < 512) copies *= 2;  // below 1024 words in all, or E
+  for (uint32_t k = threadIdx.x; k < copies * e; k += kThreads) hist[k] = 0;
+  if (threadIdx.x == 0) hist[kCountWords] = 0;
+  uint32_t* mine = hist + (threadIdx.x & (copies - 1)) * e;
+  const I* ids = (const I*)a.choices + (int64_t)i * a.c_learner + (int64_t)t0 * a.c_token;
+  const uint8_t* mask = a.mask != nullptr ? a.mask + (int64_t)i * a.mask_learner + t0 : nullptr;
+  const uint32_t top = (uint32_t)a.top, n = (uint32_t)(t1 - t0) * top;
+  constexpr int U = 8;
+  I id[U];
+  uint8_t keep[U];
+  const auto request = [&](uint32_t f0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t f = f0 + u * kThreads;  // below 2^24 + 2^13
+      const uint32_t at = f < n ? f : 0;
+      const uint32_t t = divide(at, a.top_inverse);
+      id[u] = ids[(int64_t)t * a.c_token + (at - t * top)];
+      keep[u] = 1;
+      if (mask != nullptr) keep[u] = mask[t];
+    }
+  };
+  const auto add = [&](uint32_t f0) {
+    uint32_t kept = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t f = f0 + u * kThreads;
+      const bool live = f < n && keep[u] != 0;
+      if (live && id[u] >= 0 && id[u] < (I)e) atomicAdd(&mine[(uint32_t)id[u]], 1u);
+      // a token is kept where its first choice is
+      kept += live && f - divide(f, a.top_inverse) * top == 0;
+    }
+    return kept;
+  };
+  uint32_t kept = 0;
+  if (threadIdx.x < n) request(threadIdx.x);
+  __syncthreads();
+  for (uint32_t f0 = threadIdx.x; f0 < n; f0 += U * kThreads) {
+    kept += add(f0);
+    if (f0 + U * kThreads < n) request(f0 + U * kThreads);
+  }
+  if (kept != 0) atomicAdd(&hist[kCountWords], kept);
+  __syncthreads();
+  // a thread sums the copies of its experts; only it writes hist[its experts]
+  for (uint32_t k = threadIdx.x; k < e && copies > 1; k += kThreads) {
+    uint32_t s = 0;
+#pragma unroll 4
+    for (uint32_t c = 0; c < copies; ++c) s += hist[c * e + k];
+    hist[k] = s;
+  }
+  __syncthreads();
+}
+
+template <int kThreads>
+__device__ __forceinline__ void count(const BalanceArgs& a, int i, int t0, int t1, uint32_t* hist) {
+  if (a.wide_choices != 0) count_choices<kThreads, int64_t>(a, i, t0, t1, hist);
+  else count_choices<kThreads, int32_t>(a, i, t0, t1, hist);
+}
+
+// ---------------------------------------------------------------------------
+// The pass over the logits
+// ---------------------------------------------------------------------------
+enum BalanceMode { kLossOnly = 0, kGradient = 1, kAccumulate = 2 };
+
+// A lane holds V = 16 bytes of a token's logits J times, L lanes a token, so a wave works on
+// 64 / L tokens at once.  Logits lie at any address that their type allows; 16-byte loads
+// need no more on gfx950.  Every lane loads and stores whole: a chunk that would pass the row's
+// end is moved back to end with it, and [lo, hi) are the elements that no lane before it
+// holds.  The others are computed as well and stored with the same bits, but not summed.
+// Rows narrower than V are the exception (NARROW: L = J = 1, element by element).
+template <typename T, int L, int J, bool NARROW>
+struct Chunks {
+  static constexpr int V = 16 / (int)sizeof(T);
+  typedef T vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+  int start[J], lo[J], hi, experts;
+  __device__ __forceinline__ Chunks(int lane, int e) : hi(NARROW ? e : V), experts(e) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int at = (j * L + lane) * V;
+      start[j] = NARROW ? 0 : min(at, e - V);
+      lo[j] = NARROW ? 0 : min(at - start[j], V);
+    }
+  }
+  __device__ __forceinline__ void load(const T* row, vec (&q)[J]) const {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if constexpr (NARROW) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) q[j][c] = row[min(c, experts - 1)];
+      } else {
+        q[j] = *(const vec*)(row + start[j]);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* row, const vec (&q)[J]) const {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if constexpr (NARROW) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          if (c < experts) row[c] = q[j][c];
+        }
+      } else {
+        *(vec*)(row + start[j]) = q[j];
+      }
+    }
+  }
+};
+
+// Learner i's tokens [t0, t1): their probabilities' sums into sum[experts] (LDS, kSumWords), and the
+// gradient.  before() runs once the first logits are on their way; share is read after it: (counts
+// less their mean) times the gradient's factor (LDS).  bits: where the block's kept tokens are
+// noted, if there is a mask (LDS, kBlockTokens / 32 words).
+//
+// A step is a token for every group of L lanes.  The steps of whole blocks of tokens issue the same
+// memory operations each, none of them conditional, so that a wait for one step's logits leaves
+// the loads of the next kBalanceAhead steps and the stores in flight.  The tokens that are
+// left over come first, while those loads are under way.
+template <typename T, int L, int J, bool NARROW, int MODE, int kThreads, typename F>
+__device__ __forceinline__ void pass(const BalanceArgs& a, int i, int t0, int t1, F&& before, const float* share,
+                                     double* sum, uint32_t* bits) {
+  using C = Chunks<T, L, J, NARROW>;
+  using vec = typename C::vec;
+  constexpr int V = C::V;
+  constexpr int kTokens = kThreads / L;
+  constexpr int kAhead = J == 1 ? kBalanceAhead : 1;
+  constexpr float kLog2e = 1.44269504f;
+  const int slot = threadIdx.x / L;
+  const int experts = a.experts;
+  const C ch(threadIdx.x % L, experts);
+  const bool cut = experts != L * J * V;  // some lane holds elements that are not its own
+  const int whole = (t1 - t0) / kTokens, left = (t1 - t0) % kTokens;
+  const T* x = (const T*)a.logits + (int64_t)i * a.x_learner;
+  T* grad = MODE == kLossOnly ? nullptr : (T*)a.grad + (int64_t)i * a.g_learner;
+  const bool masked = a.mask != nullptr;
+
+  vec last[J], next[kAhead + 1][J];
+  const int end = whole * kTokens + slot;
+  if (left > 0) ch.load(x + (int64_t)min(t0 + end, t1 - 1) * a.x_token, last);
+  const T* ahead = x + (int64_t)(t0 + slot) * a.x_token;
+  const int64_t step = (int64_t)kTokens * a.x_token;
+  if (whole > 0) {
+#pragma unroll
+    for (int k = 0; k <= kAhead; ++k) {
+      ch.load(ahead, next[k]);
+      ahead += k + 1 < whole ? step : 0;
+    }
+  }
+  if (masked) {
+    const uint8_t* mask = a.mask + (int64_t)i * a.mask_learner + t0;
+    for (int t = threadIdx.x; t - (int)threadIdx.x < t1 - t0; t += kThreads) {  // whole waves
+      const uint64_t word = __builtin_amdgcn_ballot_w64(t < t1 - t0 && mask[min(t, t1 - t0 - 1)] != 0);
+      if (threadIdx.x % 64 < 2) bits[t / 64 * 2 + threadIdx.x % 64] = (uint32_t)(word >> (32 * (threadIdx.x % 64)));
+    }
+    __syncthreads();
+  }
+  const auto kept = [&](int t) { return !masked || (bits[t / 32] >> (t % 32) & 1u) != 0; };
+  before();
+
+  float own[J][V];
+  if constexpr (MODE != kLossOnly) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) own[j][c] = share[NARROW ? min(c, experts - 1) : ch.start[j] + c];
+    }
+  }
+  float part[J][V] = {};
+  double total[J][V] = {};
+  const auto fold = [&]() {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        total[j][c] += (double)part[j][c];
+        part[j][c] = 0.0f;
+      }
+    }
+  };
+  // One token of each group of lanes; out: its gradient (with kAccumulate, on top of the old one).
+  const auto token = [&](const vec (&raw)[J], bool live, const T* row, vec (&out)[J]) {
+    vec old[J];
+    if constexpr (MODE == kAccumulate) ch.load(row, old);
+    float v[J][V];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) v[j][c] = (float)raw[j][c];
+    }
+    if (__builtin_amdgcn_ballot_w64(live) != ~0ull) {  // what is left out may be no number
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) v[j][c] = live ? v[j][c] : -__builtin_inff();
+      }
+    }
+    float m = v[0][0];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) m = fmaxf(m, v[j][c]);
+    }
+    m = reduce<L>(m, [](float p, float q) { return fmaxf(p, q); });
+    if (m == -__builtin_inff()) m = 0.0f;  // nothing is possible: every probability is 0
+    // exp(x - m) as 2^(x log2 e - m log2 e): the product m log2 e is rounded the same for the whole row, and
+    // below 2^20 by too little to matter to the exponential's range
+    if (__builtin_amdgcn_ballot_w64(fabsf(m) > 0x1p20f) == 0) {
+      const float shift = -(m * kLog2e);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) v[j][c] = __builtin_amdgcn_exp2f(__fmaf_rn(v[j][c], kLog2e, shift));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) v[j][c] = __builtin_amdgcn_exp2f((v[j][c] - m) * kLog2e);
+      }
+    }
+    float s = 0.0f, d = 0.0f;
+    if (cut) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          const float e = c >= ch.lo[j] && c < ch.hi ? v[j][c] : 0.0f;
+          s += e;
+          if constexpr (MODE != kLossOnly) d = __fmaf_rn(e, own[j][c], d);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          s += v[j][c];
+          if constexpr (MODE != kLossOnly) d = __fmaf_rn(v[j][c], own[j][c], d);
+        }
+      }
+    }
+    const auto add = [](float p, float q) { return p + q; };
+    s = reduce<L>(s, add);
+    if constexpr (MODE != kLossOnly) d = reduce<L>(d, add);
+    const float inv = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
+    d = -(d * inv) * inv;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        part[j][c] = __fmaf_rn(v[j][c], inv, part[j][c]);
+        if constexpr (MODE != kLossOnly) {
+          v[j][c] *= __fmaf_rn(own[j][c], inv, d);
+          if constexpr (MODE == kAccumulate) out[j][c] = live ? (T)((float)old[j][c] + v[j][c]) : old[j][c];
+          else out[j][c] = (T)v[j][c];
+        }
+      }
+    }
+  };
+  if (left > 0) {
+    vec out[J];
+    const bool there = t0 + end < t1;
+    T* row = MODE == kLossOnly ? nullptr : grad + (int64_t)(there ? t0 + end : t0) * a.g_token;
+    token(last, there && kept(there ? end : 0), row, out);
+    if constexpr (MODE != kLossOnly) {
+      if (there) ch.store(row, out);
+    }
+  }
+  T* row = MODE == kLossOnly ? nullptr : grad + (int64_t)(t0 + slot) * a.g_token;
+  const int64_t row_step = (int64_t)kTokens * a.g_token;
+  // The first loads have long arrived; once nothing is under way at the loop's start, the waits within it count
+  // the loads and stores of a round and no others.
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  int k = 0;
+  const auto go = [&](vec (&raw)[J], bool reload) {
+    vec out[J];
+    token(raw, kept(k * kTokens + slot), row, out);
+    if (reload) {
+      ch.load(ahead, raw);
+      ahead += k + kAhead + 2 < whole ? step : 0;  // past the last step its loads are repeated
+    }
+    if constexpr (MODE != kLossOnly) {
+      ch.store(row, out);
+      row += row_step;
+    }
+    if (k % kFoldTokens == kFoldTokens - 2) fold();
+    ++k;
+  };
+  while (k + kAhead < whole) {  // the loads of step k go to place k % (kAhead + 1): a move would wait for them
+#pragma unroll
+    for (int u = 0; u <= kAhead; ++u) go(next[u], true);
+  }
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    if (k < whole) go(next[u], false);
+  }
+  fold();
+  // over the wave's tokens, then the waves in order
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+#pragma unroll
+      for (int k = L; k < 64; k *= 2) total[j][c] += __shfl_xor(total[j][c], k, 64);
+    }
+  }
+  // as many waves side by side as sum has room for, then the next ones on top, then all of them in order
+  const int room = min(kThreads / 64, kSumWords / experts), wave = threadIdx.x / 64;
+  for (int w0 = 0; w0 < kThreads / 64; w0 += room) {
+    if (wave >= w0 && wave < w0 + room && threadIdx.x % 64 < L) {
+      double* to = sum + (wave - w0) * experts;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          if (c < ch.lo[j] || c >= ch.hi) continue;
+          double* q = to + ch.start[j] + c;
+          *q = w0 == 0 ? total[j][c] : *q + total[j][c];
+        }
+      }
+    }
+    __syncthreads();
+  }
+  for (int k = threadIdx.x; k < experts; k += kThreads) {
+    double t = 0.0;
+    for (int w = 0; w < room; ++w) t += sum[w * experts + k];
+    sum[k] = t;  // the thread alone reads and writes this expert's words
+  }
+  __syncthreads();
+}
+
+// The gradient's factor times the counts less their mean.  every: experts' counts (LDS).
+template <int kThreads>
+__device__ __forceinline__ void make_share(const BalanceArgs& a, double up, const uint32_t* every, uint32_t kept,
+                                           float* share, double* red) {
+  double c = 0.0;
+  for (int k = threadIdx.x; k < a.experts; k += kThreads) c += (double)every[k];
+  c = wave_sum(c);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = c;
+  __syncthreads();
+  double mean = 0.0;
+  for (int w = 0; w < kThreads / 64; ++w) mean += red[w];
+  mean /= (double)a.experts;
+  const double n = kept == 0 ? 1.0 : (double)kept;
+  const double f = a.coef * (double)a.experts / (n * n * (double)a.top) * up;
+  for (int k = threadIdx.x; k < a.experts; k += kThreads) share[k] = (float)(f * ((double)every[k] - mean));
+  __syncthreads();
+}
+
+template <typename T, int L, int J, bool NARROW, int MODE>
+__global__ __launch_bounds__(kBalanceBlock) void k_balance(const BalanceArgs a) {
+  __shared__ double sum[kSumWords];
+  __shared__ uint32_t bits[kBlockTokens / 32];
+  __shared__ float share[MODE != kLossOnly ? kMaxExperts : 1];
+  __shared__ uint32_t hist[MODE != kLossOnly ? kMaxExperts + 1 : kCountWords + 1];
+  __shared__ double red[kBalanceBlock / 64];
+  const int i = a.learner[blockIdx.y];
+  const int t0 = blockIdx.x * a.block_tokens, t1 = min(a.tokens, t0 + a.block_tokens);
+  const double up = MODE != kLossOnly && a.grad_scale != nullptr ? a.grad_scale[i] : 1.0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.tickets[blockIdx.y] = 0;  // k_balance_final's
+  pass<T, L, J, NARROW, MODE, kBalanceBlock>(a, i, t0, t1, [&] {
+    if constexpr (MODE != kLossOnly) {
+      const uint32_t* part = a.part_counts + (size_t)blockIdx.y * a.count_blocks * (a.experts + 1);
+      for (int k = threadIdx.x; k <= a.experts; k += kBalanceBlock) {
+        uint32_t s = 0;
+#pragma unroll 16
+        for (int b = 0; b < a.count_blocks; ++b) s += part[(size_t)b * (a.experts + 1) + k];
+        hist[k] = s;
+      }
+      __syncthreads();
+      make_share<kBalanceBlock>(a, up, hist, hist[a.experts], share, red);
+    } else {
+      count<kBalanceBlock>(a, i, t0, t1, hist);
+      uint32_t* out = a.part_counts + ((size_t)blockIdx.y * a.blocks + blockIdx.x) * (a.experts + 1);
+      for (int k = threadIdx.x; k < a.experts; k += kBalanceBlock) out[k] = hist[k];
+      if (threadIdx.x == 0) out[a.experts] = hist[kCountWords];
+    }
+  }, share, sum, bits);
+  double* out = a.part_probs + ((size_t)blockIdx.y * a.blocks + blockIdx.x) * a.experts;
+  for (int k = threadIdx.x; k < a.experts; k += kBalanceBlock) out[k] = sum[k];
+}
+
+// What is left to do for expert k of learner i once its sums are known; returns its part of the
+// loss, but for the loss's factor.
+__device__ __forceinline__ double finish_expert(const BalanceArgs& a, int i, int k, uint32_t count, double sum,
+                                                uint32_t kept, int64_t total) {
+  const double mean = kept == 0 ? 0.0 : sum / (double)kept;
+  a.counts[(int64_t)i * a.counts_stride + k] = (int64_t)count;
+  if (a.totals != nullptr) a.totals[(int64_t)i * a.totals_stride + k] = total + (int64_t)count;
+  if (a.means != nullptr) a.means[(int64_t)i * a.experts + k] = (float)mean;
+  return (double)count * mean;
+}
+
+__device__ __forceinline__ void write_loss(const BalanceArgs& a, int i, uint32_t kept, double sum) {
+  const double n = kept == 0 ? 1.0 : (double)kept;
+  a.loss[i] = (float)(a.coef * (double)a.experts / (n * (double)a.top) * sum);
+}
+
+template <typename T, int L, int J, bool NARROW, int MODE>
+__global__ __launch_bounds__(kBalanceOne) void k_balance_one(const BalanceArgs a) {
+  __shared__ double sum[kSumWords];
+  __shared__ uint32_t bits[kBlockTokens / 32];
+  __shared__ float share[MODE != kLossOnly ? kMaxExperts : 1];
+  __shared__ uint32_t hist[kCountWords + 1];
+  __shared__ double red[kBalanceOne / 64];
+  const int i = a.learner[blockIdx.x];
+  // read early: nothing of the call's waits for memory after the logits
+  const double up = MODE != kLossOnly && a.grad_scale != nullptr ? a.grad_scale[i] : 1.0;
+  int64_t first_total = 0;
+  if (a.totals != nullptr && (int)threadIdx.x < a.experts) first_total = a.totals[(int64_t)i * a.totals_stride + threadIdx.x];
+  const auto total = [&](int k) {
+    return k < kBalanceOne || a.totals == nullptr ? first_total : a.totals[(int64_t)i * a.totals_stride + k];
+  };
+  pass<T, L, J, NARROW, MODE, kBalanceOne>(a, i, 0, a.tokens, [&] {
+    count<kBalanceOne>(a, i, 0, a.tokens, hist);
+    if constexpr (MODE != kLossOnly) make_share<kBalanceOne>(a, up, hist, hist[kCountWords], share, red);
+  }, share, sum, bits);
+  const uint32_t kept = hist[kCountWords];
+  double l = 0.0;
+  for (int k = threadIdx.x; k < a.experts; k += kBalanceOne) l += finish_expert(a, i, k, hist[k], sum[k], kept, total(k));
+  l = wave_sum(l);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = l;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    l = 0.0;
+    for (int w = 0; w < kBalanceOne / 64; ++w) l += red[w];
+    write_loss(a, i, kept, l);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// f(lanes per token, loads per lane, whether a row is narrower than one load), lanes at least
+// kLeast: a call small enough for one block is all latency, and two widths serve it.
+template <int V, int kLeast, typename F>
+hipError_t by_lanes(int experts, F&& f) {
+  if (experts < V) return f(Int<1>(), Int<1>(), std::true_type());
+  const int l = balance_lanes(experts, V);
+  if constexpr (kLeast == 1) {
+    switch (l) {
+      case 1: return f(Int<1>(), Int<1>(), std::false_type());
+      case 2: return f(Int<2>(), Int<1>(), std::false_type());
+      case 4: return f(Int<4>(), Int<1>(), std::false_type());
+      case 16: return f(Int<16>(), Int<1>(), std::false_type());
+      case 32: return f(Int<32>(), Int<1>(), std::false_type());
+      default: break;
+    }
+  }
+  if (l <= 8) return f(Int<8>(), Int<1>(), std::false_type());
+  if (experts <= 64 * V) return f(Int<64>(), Int<1>(), std::false_type());
+  if constexpr (V == 4) {
+    if (experts > 128 * V) return f(Int<64>(), Int<4>(), std::false_type());
+  }
+  return f(Int<64>(), Int<2>(), std::false_type());
+}
+
+template <typename T, int MODE>
+hipError_t launch_pass(const BalanceArgs& a, bool one, hipStream_t s) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (one) {
+    return by_lanes<V, 8>(a.experts, [&](auto l, auto j, auto narrow) {
+      hipLaunchKernelGGL((k_balance_one<T, decltype(l)::value, decltype(j)::value, decltype(narrow)::value, MODE>),
+                         dim3(a.n_present), dim3(kBalanceOne), 0, s, a);
+      return hipGetLastError();
+    });
+  }
+  return by_lanes<V, 1>(a.experts, [&](auto l, auto j, auto narrow) {
+    hipLaunchKernelGGL((k_balance<T, decltype(l)::value, decltype(j)::value, decltype(narrow)::value, MODE>),
+                       dim3(a.blocks, a.n_present), dim3(kBalanceBlock), 0, s, a);
+    return hipGetLastError();
+  });
+}
+
+template <typename T>
+hipError_t launch_typed(const BalanceArgs& a, bool one, hipStream_t s) {
+  if (a.grad == nullptr) return launch_pass<T, kLossOnly>(a, one, s);
+  return a.accumulate != 0 ? launch_pass<T, kAccumulate>(a, one, s) : launch_pass<T, kGradient>(a, one, s);
+}
+
+}  // namespace
+}  // namespace dlc

@@ -12,11 +12,22 @@ namespace dlc {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 64;
-constexpr int kBalanceBlock = 512;       // threads of a block over the logits
-constexpr int kBalanceOne = 1024;        // threads of the block that does a learner's whole call
+#ifndef VB
+#define VB 256
+#define VA 2
+#define VS 2048
+#endif
+constexpr int kBalanceBlock = VB;       // threads of a block over the logits
+constexpr int kBalanceAhead = VA;
+constexpr int kBalanceOne = 512;         // threads of the block that does a learner's whole call
 constexpr int kCountBlock = 512;
+constexpr int kFinalBlock = 512;
+constexpr int kFinalExperts = 32;        // experts of a block of the final sums
+constexpr int kFinalMost = kMaxExperts / kFinalExperts;
 constexpr int kFoldTokens = 16;          // tokens a lane sums in fp32 before it goes on in fp64
-constexpr int kCountWords = 4096;        // LDS words of a block's histogram copies
+constexpr int kCountWords = 1024;        // LDS words of a block's histogram copies
+constexpr int kSumWords = VS;          // LDS words of the waves' probability sums
+constexpr int kBlockTokens = 16384;      // most tokens of a block over the logits
 constexpr int64_t kCountTokens = 1 << 18;  // most tokens of a counting block, see divide()
 
 struct BalanceArgs {
@@ -37,6 +48,8 @@ struct BalanceArgs {
   int64_t totals_stride;
   uint32_t* part_counts;      // [present][count_blocks][experts + 1]: counts, kept tokens
   double* part_probs;         // [present][blocks][experts] sums of probabilities
+  double* part_loss;          // [present][kFinalMost]
+  uint32_t* tickets;          // [present]
   double coef;
   int32_t tokens, experts, top;
   uint32_t top_inverse;       // ceil(2^32 / top), 0 for top = 1
@@ -63,12 +76,26 @@ struct WeightArgs {
 
 static_assert(sizeof(BalanceArgs) <= 4096 && sizeof(WeightArgs) <= 4096);
 
+// Lanes per token: the fewest that hold a row in one load of v elements each, 64 at most.
+inline int balance_lanes(int experts, int v) {
+  int l = 1;
+  while (l < 64 && l * v < experts) l *= 2;
+  return l;
+}
+
 // Kernel launchers (dlc_experts.hip).  Each returns hipSuccess or the launch error.
-// one kernel, a block per learner
-hipError_t launch_balance_one(const BalanceArgs& a, int32_t type, hipStream_t s);
 hipError_t launch_balance_count(const BalanceArgs& a, hipStream_t s);
-// with a gradient after launch_balance_count; without one it counts its own tokens' choices
-hipError_t launch_balance(const BalanceArgs& a, int32_t type, hipStream_t s);
+// One block per learner for the whole call, or the pass over the logits: with a gradient after
+// launch_balance_count; without one it counts its own tokens' choices.
+hipError_t launch_balance(const BalanceArgs& a, int32_t type, bool one, hipStream_t s);
+template <int32_t kType>
+hipError_t launch_balance_of(const BalanceArgs& a, bool one, hipStream_t s);  // dlc_balance_*.hip
+template <>
+hipError_t launch_balance_of<kF32>(const BalanceArgs& a, bool one, hipStream_t s);
+template <>
+hipError_t launch_balance_of<kBF16>(const BalanceArgs& a, bool one, hipStream_t s);
+template <>
+hipError_t launch_balance_of<kF16>(const BalanceArgs& a, bool one, hipStream_t s);
 hipError_t launch_balance_final(const BalanceArgs& a, hipStream_t s);
 // tokens that a block of `threads` threads takes at once
 int32_t balance_tokens(int32_t type, int32_t experts, int32_t threads);

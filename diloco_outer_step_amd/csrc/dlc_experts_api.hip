@@ -24,9 +24,14 @@ using dlc::round256;
 static_assert(dlc::kMaxExperts == DLC_MAX_EXPERTS && dlc::kMaxChoices == DLC_MAX_CHOICES);
 static_assert((dlc::kCountTokens - 1) * (int64_t)DLC_MAX_CHOICES * (DLC_MAX_CHOICES - 1) < (int64_t(1) << 32));
 
-constexpr int64_t kBalanceBlocks = 1024;   // over the logits, all learners
-constexpr int64_t kMinSteps = 4;           // of a block over the logits
-constexpr int64_t kCountChoices = 8192;    // choices of a counting block
+#ifndef VN
+#define VN 1024
+#define VM 2
+#define VC 4096
+#endif
+constexpr int64_t kBalanceBlocks = VN;   // over the logits, all learners
+constexpr int64_t kMinSteps = VM;           // of a block over the logits
+constexpr int64_t kCountChoices = VC;    // choices of a counting block
 constexpr int64_t kMaxCountBlocks = 32;    // per learner, as long as a block's tokens stay below kCountTokens
 constexpr int64_t kMaxStride = int64_t(1) << 48;
 
@@ -36,6 +41,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t kOneLogits = 16384, kOneChoices = 16384;
 
 bool one_block(int64_t tokens, int64_t experts, int64_t top) {
+  static_assert(kOneLogits <= dlc::kBlockTokens);
   return tokens * experts <= kOneLogits && tokens * top <= kOneChoices;
 }
 
@@ -49,7 +55,7 @@ BalancePartition balance_partition(int64_t tokens, int32_t experts, int64_t top,
   const int64_t step = dlc::balance_tokens(type, experts, dlc::kBalanceBlock);
   const int64_t most = std::max<int64_t>(1, kBalanceBlocks / present);
   p.block_tokens = std::max(kMinSteps * step, ceil_div(ceil_div(tokens, most), step) * step);
-  p.block_tokens = std::min(p.block_tokens, dlc::kCountTokens);
+  p.block_tokens = std::min<int64_t>(p.block_tokens, dlc::kBlockTokens);
   p.blocks = std::max<int64_t>(1, ceil_div(tokens, p.block_tokens));
   p.count_blocks = p.blocks;
   p.count_tokens = p.block_tokens;
@@ -67,6 +73,10 @@ size_t probs_bytes(const BalancePartition& p, int32_t experts, int32_t present) 
 
 size_t counts_bytes(const BalancePartition& p, int32_t experts, int32_t present) {
   return round256((size_t)present * p.count_blocks * (experts + 1) * sizeof(uint32_t));
+}
+
+size_t loss_bytes(int32_t present) {
+  return round256((size_t)present * (dlc::kFinalMost * sizeof(double) + sizeof(uint32_t)));
 }
 
 int32_t check_sizes(int32_t n_learners, int64_t n_tokens, int32_t n_experts) {
@@ -115,7 +125,7 @@ int32_t dlc_expert_balance_workspace_bytes(int32_t n_learners, int64_t n_tokens,
       for (const int32_t type : {DLC_FLOAT32, DLC_BFLOAT16}) {
         for (const bool gradient : {false, true}) {
           const BalancePartition p = balance_partition(n_tokens, n_experts, DLC_MAX_CHOICES, type, present, gradient);
-          most = std::max(most, probs_bytes(p, n_experts, present) + counts_bytes(p, n_experts, present));
+          most = std::max(most, probs_bytes(p, n_experts, present) + counts_bytes(p, n_experts, present) + loss_bytes(present));
         }
       }
     }
@@ -180,7 +190,8 @@ int32_t dlc_expert_balance(const void* logits, int32_t logits_type, int64_t logi
     const BalancePartition p =
         balance_partition(n_tokens, n_experts, n_choices, logits_type, a.n_present, gradient);
     const size_t probs = probs_bytes(p, n_experts, a.n_present);
-    const size_t need = one ? 0 : probs + counts_bytes(p, n_experts, a.n_present);
+    const size_t losses = probs + counts_bytes(p, n_experts, a.n_present);
+    const size_t need = one ? 0 : losses + loss_bytes(a.n_present);
     if (workspace == nullptr || workspace_bytes < need)
       return fail(DLC_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
     if (!aligned256(workspace)) return fail(DLC_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
@@ -219,6 +230,8 @@ int32_t dlc_expert_balance(const void* logits, int32_t logits_type, int64_t logi
     a.totals_stride = totals_stride;
     a.part_probs = static_cast<double*>(workspace);
     a.part_counts = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + probs);
+    a.part_loss = reinterpret_cast<double*>(static_cast<char*>(workspace) + losses);
+    a.tickets = reinterpret_cast<uint32_t*>(a.part_loss + (size_t)a.n_present * dlc::kFinalMost);
     a.coef = coef;
     a.tokens = (int32_t)n_tokens;
     a.experts = n_experts;
@@ -231,10 +244,10 @@ int32_t dlc_expert_balance(const void* logits, int32_t logits_type, int64_t logi
     const hipStream_t st = static_cast<hipStream_t>(hip_stream);
     hipError_t e;
     if (one) {
-      e = dlc::launch_balance_one(a, logits_type, st);
+      e = dlc::launch_balance(a, logits_type, true, st);
     } else {
       e = gradient ? dlc::launch_balance_count(a, st) : hipSuccess;
-      if (e == hipSuccess) e = dlc::launch_balance(a, logits_type, st);
+      if (e == hipSuccess) e = dlc::launch_balance(a, logits_type, false, st);
       if (e == hipSuccess) e = dlc::launch_balance_final(a, st);
     }
     return e != hipSuccess ? hip_fail(e, "balance kernel launch") : ok();
