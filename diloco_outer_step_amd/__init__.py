@@ -884,37 +884,74 @@ def dlc_expert_balance(logits, choices, loss, counts, workspace, coef=1.0, mask=
     [K, E], grad_logits like logits (added to with `accumulate`), totals int64 [K, E] (added to).
     grad_scale: device fp64 [K], the factor of the gradient.  logits, choices, mask, grad_logits,
     counts and totals may be views with a dense last dimension."""
+    k, t, e, top, (xl, xt, cl, ct, ns, ml, ts, gl, gt) = _balance_views(
+        logits, choices, loss, counts, workspace, mask, mean_probs, grad_logits, grad_scale, totals)
+    pres = _presence(present, k)
+    _on_device(logits.get_device(), stream, _lib.dlc_expert_balance, logits.data_ptr(), _FLOAT_TYPES[logits.dtype], xl,
+               xt, choices.data_ptr(), _CHOICE_TYPES[choices.dtype], cl, ct, _address(mask), ml, k, pres, t, e, top,
+               float(coef), loss.data_ptr(), counts.data_ptr(), ns, _address(mean_probs), _address(totals), ts,
+               _address(grad_logits), gl, gt, _address(grad_scale), DLC_ACCUMULATE if accumulate else 0,
+               workspace.data_ptr(), workspace.numel())
+
+
+def _balance_views(logits, choices, loss, counts, workspace, mask, mean_probs, grad_logits, grad_scale, totals):
+    """Checks of a balance call's buffers -> K, T, E, top and the strides of the views.  As in _check_buffers: one
+    pass of plain tests, the naming checks only where it fails."""
+    try:
+        dev, shape, kind = logits.get_device(), logits.shape, logits.dtype
+        k, t, e = shape
+        rows, per = (k, e), (k,)
+        xl, xt, x1 = logits.stride()
+        cl, ct, c1 = choices.stride()
+        ns, n1 = counts.stride()
+        _, tokens, top = chosen = choices.shape
+        one = e <= 1
+        ok = (dev >= 0 and kind in _FLOAT_TYPES and (x1 == 1 or one) and choices.dtype in _CHOICE_TYPES
+              and chosen[0] == k and tokens == t and (c1 == 1 or top <= 1) and choices.get_device() == dev
+              and counts.dtype is torch.int64 and counts.shape == rows and (n1 == 1 or one) and counts.get_device() == dev
+              and loss.dtype is torch.float32 and loss.shape == per and loss.is_contiguous() and loss.get_device() == dev
+              and workspace.dtype is torch.uint8 and workspace.is_contiguous() and workspace.get_device() == dev)
+        ml = ts = gl = gt = 0
+        if ok and mask is not None:
+            ml, m1 = mask.stride()
+            ok = (mask.dtype in _MASK_TYPES and mask.shape == (k, t) and (m1 == 1 or t <= 1) and mask.get_device() == dev)
+        if ok and totals is not None:
+            ts, t1 = totals.stride()
+            ok = (totals.dtype is torch.int64 and totals.shape == rows and (t1 == 1 or one) and totals.get_device() == dev)
+        if ok and grad_logits is not None:
+            gl, gt, g1 = grad_logits.stride()
+            ok = (grad_logits.dtype is kind and grad_logits.shape == shape and (g1 == 1 or one)
+                  and grad_logits.get_device() == dev)
+        if ok and mean_probs is not None:
+            ok = (mean_probs.dtype is torch.float32 and mean_probs.shape == rows and mean_probs.is_contiguous()
+                  and mean_probs.get_device() == dev)
+        if ok and grad_scale is not None:
+            ok = (grad_scale.dtype is torch.float64 and grad_scale.shape == per and grad_scale.is_contiguous()
+                  and grad_scale.get_device() == dev)
+        if ok:
+            return k, t, e, top, (xl, xt, cl, ct, ns, ml, ts, gl, gt)
+    except (AttributeError, TypeError, ValueError, IndexError):
+        pass
     if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
         raise ValueError("logits must be a [K, T, E] tensor")
     if not isinstance(choices, torch.Tensor) or choices.dim() != 3:
         raise ValueError("choices must be a [K, T, top] tensor")
     k, t, e = shape = logits.shape
-    xl, xt = _view(logits, "logits", _FLOAT_TYPES, shape)
-    cl, ct = _view(choices, "choices", _CHOICE_TYPES, (k, t, choices.shape[2]))
-    ns, = _view(counts, "counts", (torch.int64,), (k, e))
-    ml = ts = gl = gt = 0
     bufs = [("loss", loss, torch.float32, (k,)), ("workspace", workspace, torch.uint8, None)]
-    views = [("logits", logits), ("choices", choices), ("counts", counts)]
-    if mask is not None:
-        ml, = _view(mask, "mask", _MASK_TYPES, (k, t))
-        views.append(("mask", mask))
-    if totals is not None:
-        ts, = _view(totals, "totals", (torch.int64,), (k, e))
-        views.append(("totals", totals))
-    if grad_logits is not None:
-        gl, gt = _view(grad_logits, "grad_logits", (logits.dtype,), shape)
-        views.append(("grad_logits", grad_logits))
     if mean_probs is not None:
         bufs.append(("mean_probs", mean_probs, torch.float32, (k, e)))
     if grad_scale is not None:
         bufs.append(("grad_scale", grad_scale, torch.float64, (k,)))
-    pres = _presence(present, k)
-    _check_views(bufs, views)
-    _on_device(logits.get_device(), stream, _lib.dlc_expert_balance, logits.data_ptr(), _FLOAT_TYPES[logits.dtype], xl,
-               xt, choices.data_ptr(), _CHOICE_TYPES[choices.dtype], cl, ct, _address(mask), ml, k, pres, t, e,
-               choices.shape[2], float(coef), loss.data_ptr(), counts.data_ptr(), ns, _address(mean_probs),
-               _address(totals), ts, _address(grad_logits), gl, gt, _address(grad_scale),
-               DLC_ACCUMULATE if accumulate else 0, workspace.data_ptr(), workspace.numel())
+    views = [("logits", logits, _FLOAT_TYPES, shape),
+             ("choices", choices, _CHOICE_TYPES, (k, t, choices.shape[2])), ("counts", counts, (torch.int64,), (k, e))]
+    for name, v, types, shape in (("mask", mask, _MASK_TYPES, (k, t)), ("totals", totals, (torch.int64,), (k, e)),
+                                  ("grad_logits", grad_logits, (logits.dtype,), shape)):
+        if v is not None:
+            views.append((name, v, types, shape))
+    for view in views:
+        _view(view[1], view[0], *view[2:])
+    _check_views(bufs, [view[:2] for view in views])
+    raise ValueError("the call's buffers do not fit together")
 
 
 def _check_views(bufs, views):

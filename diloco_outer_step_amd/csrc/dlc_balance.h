@@ -18,19 +18,12 @@
 namespace dlc {
 namespace {
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
-}
-
 // f of v and of the other half's value, for each group of L lanes whose halves hold one value
 // each.  Within rows of 16 lanes the other half is read by the instruction that uses it;
 // rows are exchanged by a swap of which both results are used.
-template <int L, typename F>
-__device__ __forceinline__ float with_other_half(float v, F&& f) {
-  const int x = __builtin_bit_cast(int, v);
-  int y = x, z = x;
+template <int L>
+__device__ __forceinline__ void exchange(int x, int& y, int& z) {
+  y = z = x;
   if constexpr (L == 2) y = __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true);    // quad 1 0 3 2
   if constexpr (L == 4) y = __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true);    // quad 2 3 0 1
   if constexpr (L == 8) y = __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true);   // half row mirrored
@@ -45,11 +38,22 @@ __device__ __forceinline__ float with_other_half(float v, F&& f) {
     y = (int)r[0];
     z = (int)r[1];
   }
-  return f(__builtin_bit_cast(float, z), __builtin_bit_cast(float, y));
 }
 
-template <int L, typename F>
-__device__ __forceinline__ float reduce(float v, F&& f) {
+template <int L, typename T, typename F>
+__device__ __forceinline__ T with_other_half(T v, F&& f) {
+  int y[sizeof(T) / 4], z[sizeof(T) / 4], x[sizeof(T) / 4];
+  __builtin_memcpy(x, &v, sizeof(T));
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(T) / 4; ++k) exchange<L>(x[k], y[k], z[k]);
+  T p, q;
+  __builtin_memcpy(&p, z, sizeof(T));
+  __builtin_memcpy(&q, y, sizeof(T));
+  return f(p, q);
+}
+
+template <int L, typename T, typename F>
+__device__ __forceinline__ T reduce(T v, F&& f) {
   if constexpr (L >= 2) v = with_other_half<2>(v, f);
   if constexpr (L >= 4) v = with_other_half<4>(v, f);
   if constexpr (L >= 8) v = with_other_half<8>(v, f);
@@ -57,6 +61,10 @@ __device__ __forceinline__ float reduce(float v, F&& f) {
   if constexpr (L >= 32) v = with_other_half<32>(v, f);
   if constexpr (L >= 64) v = with_other_half<64>(v, f);
   return v;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+  return reduce<64>(v, [](double p, double q) { return p + q; });
 }
 
 // ---------------------------------------------------------------------------
@@ -68,8 +76,8 @@ __device__ __forceinline__ uint32_t divide(uint32_t f, uint32_t inverse) {
   return inverse == 0 ? f : __umulhi(f, inverse);
 }
 
-// A learner's choices of tokens [t0, t1) -> hist[0 .. experts), kept tokens -> hist[experts].
-// The words of hist hold copies of the histogram, so that lanes with the same choice (routers
+// A learner's choices of tokens [t0, t1) -> hist[0 .. experts), kept tokens -> hist[kCountWords],
+// choices that count for some expert -> hist[kCountWords + 1].  The words of hist hold copies of the histogram, so that lanes with the same choice (routers
 // have favourites, and few experts) add to different words: 16 at most, which are summed
 // at the end.
 template <int kThreads, typename I>
@@ -78,45 +86,50 @@ __device__ __forceinline__ void count_choices(const BalanceArgs& a, int i, int t
   uint32_t copies = 1;
   while (copies < 16 && copies * e < 512) copies *= 2;  // below 1024 words in all, or E
   for (uint32_t k = threadIdx.x; k < copies * e; k += kThreads) hist[k] = 0;
-  if (threadIdx.x == 0) hist[kCountWords] = 0;
+  if (threadIdx.x < 2) hist[kCountWords + threadIdx.x] = 0;
   uint32_t* mine = hist + (threadIdx.x & (copies - 1)) * e;
   const I* ids = (const I*)a.choices + (int64_t)i * a.c_learner + (int64_t)t0 * a.c_token;
   const uint8_t* mask = a.mask != nullptr ? a.mask + (int64_t)i * a.mask_learner + t0 : nullptr;
   const uint32_t top = (uint32_t)a.top, n = (uint32_t)(t1 - t0) * top;
   constexpr int U = 8;
   I id[U];
-  uint8_t keep[U];
+  uint32_t live = 0, first = 0;  // bit u: choice u counts, is its token's first (so the token is kept)
   const auto request = [&](uint32_t f0) {
+    live = first = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t f = f0 + u * kThreads;  // below 2^24 + 2^13
       const uint32_t at = f < n ? f : 0;
-      const uint32_t t = divide(at, a.top_inverse);
-      id[u] = ids[(int64_t)t * a.c_token + (at - t * top)];
-      keep[u] = 1;
-      if (mask != nullptr) keep[u] = mask[t];
+      const uint32_t t = divide(at, a.top_inverse), j = at - t * top;
+      id[u] = ids[(int64_t)t * a.c_token + j];
+      bool keep = f < n;
+      if (mask != nullptr) keep = keep && mask[t] != 0;
+      live |= keep ? 1u << u : 0;
+      first |= keep && j == 0 ? 1u << u : 0;
     }
   };
-  const auto add = [&](uint32_t f0) {
-    uint32_t kept = 0;
+  uint32_t kept = 0, valid = 0;
+  const auto add = [&]() {
+    kept += __popc(first);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t f = f0 + u * kThreads;
-      const bool live = f < n && keep[u] != 0;
-      if (live && id[u] >= 0 && id[u] < (I)e) atomicAdd(&mine[(uint32_t)id[u]], 1u);
-      // a token is kept where its first choice is
-      kept += live && f - divide(f, a.top_inverse) * top == 0;
+      if ((live >> u & 1u) != 0 && (std::make_unsigned_t<I>)id[u] < e) {
+        atomicAdd(&mine[(uint32_t)id[u]], 1u);
+        ++valid;
+      }
     }
-    return kept;
   };
-  uint32_t kept = 0;
   if (threadIdx.x < n) request(threadIdx.x);
   __syncthreads();
   for (uint32_t f0 = threadIdx.x; f0 < n; f0 += U * kThreads) {
-    kept += add(f0);
+    add();
     if (f0 + U * kThreads < n) request(f0 + U * kThreads);
   }
-  if (kept != 0) atomicAdd(&hist[kCountWords], kept);
+  // a lane per wave adds (of 64 lanes at one address the compiler makes a loop)
+  const auto sum = [](uint32_t p, uint32_t q) { return p + q; };
+  kept = reduce<64>(kept, sum);
+  valid = reduce<64>(valid, sum);
+  if (threadIdx.x % 64 < 2) atomicAdd(&hist[kCountWords + threadIdx.x % 64], threadIdx.x % 64 == 0 ? kept : valid);
   __syncthreads();
   // a thread sums the copies of its experts; only it writes hist[its experts]
   for (uint32_t k = threadIdx.x; k < e && copies > 1; k += kThreads) {
@@ -144,8 +157,10 @@ enum BalanceMode { kLossOnly = 0, kGradient = 1, kAccumulate = 2 };
 // need no more on gfx950.  Every lane loads and stores whole: a chunk that would pass the row's
 // end is moved back to end with it, and [lo, hi) are the elements that no lane before it
 // holds.  The others are computed as well and stored with the same bits, but not summed.
-// Rows narrower than V are the exception (NARROW: L = J = 1, element by element).
-template <typename T, int L, int J, bool NARROW>
+// Rows narrower than V are the exception (NARROW: L = J = 1, element by element).  STREAM: not to be
+// kept in the caches, which is faster by 5% of the call where the gradient is written too (32768 x
+// 256 x 8 bf16: 68.3 against 72.0 us) and slower by 4% where it is not.
+template <typename T, int L, int J, bool NARROW, bool STREAM>
 struct Chunks {
   static constexpr int V = 16 / (int)sizeof(T);
   typedef T vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
@@ -165,7 +180,7 @@ struct Chunks {
 #pragma unroll
         for (int c = 0; c < V; ++c) q[j][c] = row[min(c, experts - 1)];
       } else {
-        q[j] = *(const vec*)(row + start[j]);
+        q[j] = STREAM ? __builtin_nontemporal_load((const vec*)(row + start[j])) : *(const vec*)(row + start[j]);
       }
     }
   }
@@ -178,25 +193,38 @@ struct Chunks {
           if (c < experts) row[c] = q[j][c];
         }
       } else {
-        *(vec*)(row + start[j]) = q[j];
+        if constexpr (STREAM) __builtin_nontemporal_store(q[j], (vec*)(row + start[j]));
+        else *(vec*)(row + start[j]) = q[j];
       }
     }
   }
 };
 
-// Learner i's tokens [t0, t1): their probabilities' sums into sum[experts] (LDS, kSumWords), and the
-// gradient.  before() runs once the first logits are on their way; share is read after it: (counts
-// less their mean) times the gradient's factor (LDS).  bits: where the block's kept tokens are
-// noted, if there is a mask (LDS, kBlockTokens / 32 words).
+// LDS of a block over the logits.
+template <typename T, int kThreads>
+struct Work {
+  union {
+    float share[kMaxExperts];                          // (counts less their mean) times the gradient's factor
+    double sums[16 / sizeof(T) * (kThreads + 8)];      // the lanes' sums of probabilities, once share has been read
+  };
+  double stage[kThreads];
+  uint32_t bits[kBlockTokens / 32];                    // the block's kept tokens, if there is a mask
+  uint32_t hist[kCountWords + 2];
+  double red[kThreads / 64];
+};
+
+// Learner i's tokens [t0, t1): the gradient, and emit(k, sum of the probabilities of expert k), by one
+// thread for each expert.  before() runs once the first logits are on their way; work.share is read
+// after it.
 //
 // A step is a token for every group of L lanes.  The steps of whole blocks of tokens issue the same
 // memory operations each, none of them conditional, so that a wait for one step's logits leaves
 // the loads of the next kBalanceAhead steps and the stores in flight.  The tokens that are
 // left over come first, while those loads are under way.
-template <typename T, int L, int J, bool NARROW, int MODE, int kThreads, typename F>
-__device__ __forceinline__ void pass(const BalanceArgs& a, int i, int t0, int t1, F&& before, const float* share,
-                                     double* sum, uint32_t* bits) {
-  using C = Chunks<T, L, J, NARROW>;
+template <typename T, int L, int J, bool NARROW, int MODE, int kThreads, typename F, typename G>
+__device__ __forceinline__ void pass(const BalanceArgs& a, int i, int t0, int t1, F&& before, G&& emit,
+                                     Work<T, kThreads>& work) {
+  using C = Chunks<T, L, J, NARROW, MODE != kLossOnly>;
   using vec = typename C::vec;
   constexpr int V = C::V;
   constexpr int kTokens = kThreads / L;
@@ -227,11 +255,11 @@ __device__ __forceinline__ void pass(const BalanceArgs& a, int i, int t0, int t1
     const uint8_t* mask = a.mask + (int64_t)i * a.mask_learner + t0;
     for (int t = threadIdx.x; t - (int)threadIdx.x < t1 - t0; t += kThreads) {  // whole waves
       const uint64_t word = __builtin_amdgcn_ballot_w64(t < t1 - t0 && mask[min(t, t1 - t0 - 1)] != 0);
-      if (threadIdx.x % 64 < 2) bits[t / 64 * 2 + threadIdx.x % 64] = (uint32_t)(word >> (32 * (threadIdx.x % 64)));
+      if (threadIdx.x % 64 < 2) work.bits[t / 64 * 2 + threadIdx.x % 64] = (uint32_t)(word >> (32 * (threadIdx.x % 64)));
     }
     __syncthreads();
   }
-  const auto kept = [&](int t) { return !masked || (bits[t / 32] >> (t % 32) & 1u) != 0; };
+  const auto kept = [&](int t) { return !masked || (work.bits[t / 32] >> (t % 32) & 1u) != 0; };
   before();
 
   float own[J][V];
@@ -239,7 +267,7 @@ __device__ __forceinline__ void pass(const BalanceArgs& a, int i, int t0, int t1
 #pragma unroll
     for (int j = 0; j < J; ++j) {
 #pragma unroll
-      for (int c = 0; c < V; ++c) own[j][c] = share[NARROW ? min(c, experts - 1) : ch.start[j] + c];
+      for (int c = 0; c < V; ++c) own[j][c] = work.share[NARROW ? min(c, experts - 1) : ch.start[j] + c];
     }
   }
   float part[J][V] = {};
@@ -372,89 +400,118 @@ __device__ __forceinline__ void pass(const BalanceArgs& a, int i, int t0, int t1
     if (k < whole) go(next[u], false);
   }
   fold();
-  // over the wave's tokens, then the waves in order
+  // Every lane's sums to LDS (a pitch that lets two lanes at most of each 32 meet in a bank), then for each expert
+  // kSlices threads over the groups of lanes, then one over those threads.
+  constexpr int kPitch = kThreads + 8, kWidth = L * V, kGroups = kThreads / L;
+  constexpr int kSlices = kWidth < kThreads ? kThreads / kWidth : 1;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
+    __syncthreads();  // share, or the last sums, have been read
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
+    for (int c = 0; c < V; ++c) work.sums[c * kPitch + threadIdx.x] = total[j][c];
+    __syncthreads();
+    for (int q = threadIdx.x % (kSlices * kWidth); q < kSlices * kWidth; q += kThreads) {
+      const int slice = q / kWidth, l = q % kWidth / V, k = j * kWidth + q % kWidth;
+      const int c = NARROW || k >= experts ? q % V : k - min((j * L + l) * V, experts - V);
+      double s = 0.0;
 #pragma unroll
-      for (int k = L; k < 64; k *= 2) total[j][c] += __shfl_xor(total[j][c], k, 64);
-    }
-  }
-  // as many waves side by side as sum has room for, then the next ones on top, then all of them in order
-  const int room = min(kThreads / 64, kSumWords / experts), wave = threadIdx.x / 64;
-  for (int w0 = 0; w0 < kThreads / 64; w0 += room) {
-    if (wave >= w0 && wave < w0 + room && threadIdx.x % 64 < L) {
-      double* to = sum + (wave - w0) * experts;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-          if (c < ch.lo[j] || c >= ch.hi) continue;
-          double* q = to + ch.start[j] + c;
-          *q = w0 == 0 ? total[j][c] : *q + total[j][c];
-        }
+      for (int g = 0; g < kGroups / kSlices; ++g) s += work.sums[c * kPitch + (slice * (kGroups / kSlices) + g) * L + l];
+      if constexpr (kSlices == 1) {
+        if (k < experts) emit(k, s);
+      } else {
+        work.stage[q] = s;
       }
     }
-    __syncthreads();
+    if constexpr (kSlices > 1) {
+      __syncthreads();
+      const int k = j * kWidth + threadIdx.x;
+      if ((int)threadIdx.x < kWidth && k < experts) {
+        double s = 0.0;
+#pragma unroll
+        for (int q = 0; q < kSlices; ++q) s += work.stage[q * kWidth + threadIdx.x];
+        emit(k, s);
+      }
+    }
   }
-  for (int k = threadIdx.x; k < experts; k += kThreads) {
-    double t = 0.0;
-    for (int w = 0; w < room; ++w) t += sum[w * experts + k];
-    sum[k] = t;  // the thread alone reads and writes this expert's words
-  }
+}
+
+// The gradient's factor times the counts less their mean.  hist: counts, and in its last two words
+// kept tokens and choices in all.
+template <int kThreads>
+__device__ __forceinline__ void make_share(const BalanceArgs& a, double up, const uint32_t* hist, float* share) {
+  const uint32_t kept = hist[kCountWords];
+  const double mean = (double)hist[kCountWords + 1] / (double)a.experts;
+  const double n = kept == 0 ? 1.0 : (double)kept;
+  const double f = a.coef * (double)a.experts / (n * n * (double)a.top) * up;
+  for (int k = threadIdx.x; k < a.experts; k += kThreads) share[k] = (float)(f * ((double)hist[k] - mean));
   __syncthreads();
 }
 
-// The gradient's factor times the counts less their mean.  every: experts' counts (LDS).
+// Rows of part_counts summed in one column, 16 loads under way at a time.
+__device__ __forceinline__ uint32_t sum_column(const uint32_t* p, int pitch, int rows) {
+  uint32_t s = 0;
+  int b = 0;
+  for (; b + 16 <= rows; b += 16) {
+    uint32_t v[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) v[u] = p[(size_t)(b + u) * pitch];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) s += v[u];
+  }
+#pragma unroll 4
+  for (; b < rows; ++b) s += p[(size_t)b * pitch];
+  return s;
+}
+
+// A row of part_counts from hist: the counts, kept tokens, choices in all.
 template <int kThreads>
-__device__ __forceinline__ void make_share(const BalanceArgs& a, double up, const uint32_t* every, uint32_t kept,
-                                           float* share, double* red) {
-  double c = 0.0;
-  for (int k = threadIdx.x; k < a.experts; k += kThreads) c += (double)every[k];
-  c = wave_sum(c);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = c;
-  __syncthreads();
-  double mean = 0.0;
-  for (int w = 0; w < kThreads / 64; ++w) mean += red[w];
-  mean /= (double)a.experts;
-  const double n = kept == 0 ? 1.0 : (double)kept;
-  const double f = a.coef * (double)a.experts / (n * n * (double)a.top) * up;
-  for (int k = threadIdx.x; k < a.experts; k += kThreads) share[k] = (float)(f * ((double)every[k] - mean));
-  __syncthreads();
+__device__ __forceinline__ void write_counts(const BalanceArgs& a, uint32_t* out, const uint32_t* hist) {
+  for (int k = threadIdx.x; k < a.experts; k += kThreads) out[k] = hist[k];
+  if (threadIdx.x < 2) out[a.experts + threadIdx.x] = hist[kCountWords + threadIdx.x];
 }
 
 template <typename T, int L, int J, bool NARROW, int MODE>
 __global__ __launch_bounds__(kBalanceBlock) void k_balance(const BalanceArgs a) {
-  __shared__ double sum[kSumWords];
-  __shared__ uint32_t bits[kBlockTokens / 32];
-  __shared__ float share[MODE != kLossOnly ? kMaxExperts : 1];
-  __shared__ uint32_t hist[MODE != kLossOnly ? kMaxExperts + 1 : kCountWords + 1];
-  __shared__ double red[kBalanceBlock / 64];
-  const int i = a.learner[blockIdx.y];
+  __shared__ Work<T, kBalanceBlock> work;
+  const int i = a.learner[blockIdx.y], row = a.experts + 2;
   const int t0 = blockIdx.x * a.block_tokens, t1 = min(a.tokens, t0 + a.block_tokens);
   const double up = MODE != kLossOnly && a.grad_scale != nullptr ? a.grad_scale[i] : 1.0;
   if (blockIdx.x == 0 && threadIdx.x == 0) a.tickets[blockIdx.y] = 0;  // k_balance_final's
+  const uint32_t* part = a.part_counts + (size_t)blockIdx.y * a.count_blocks * row;
+  double* out = a.part_probs + ((size_t)blockIdx.y * a.blocks + blockIdx.x) * a.experts;
+  double loss = 0.0;
   pass<T, L, J, NARROW, MODE, kBalanceBlock>(a, i, t0, t1, [&] {
-    if constexpr (MODE != kLossOnly) {
-      const uint32_t* part = a.part_counts + (size_t)blockIdx.y * a.count_blocks * (a.experts + 1);
-      for (int k = threadIdx.x; k <= a.experts; k += kBalanceBlock) {
-        uint32_t s = 0;
-#pragma unroll 16
-        for (int b = 0; b < a.count_blocks; ++b) s += part[(size_t)b * (a.experts + 1) + k];
-        hist[k] = s;
+    if (MODE == kLossOnly || a.count_blocks == 1) {
+      // the gradient needs all of the learner's counts: every block counts for itself where that is little work
+      if constexpr (MODE == kLossOnly) count<kBalanceBlock>(a, i, t0, t1, work.hist);
+      else count<kBalanceBlock>(a, i, 0, a.tokens, work.hist);
+      if (MODE == kLossOnly || blockIdx.x == 0)
+        write_counts<kBalanceBlock>(a, a.part_counts + ((size_t)blockIdx.y * a.count_blocks + blockIdx.x) * row, work.hist);
+    } else {
+      for (int k = threadIdx.x; k < a.experts; k += kBalanceBlock) work.hist[k] = sum_column(part + k, row, a.count_blocks);
+      if (threadIdx.x < 128) {  // a wave for the kept tokens, one for the choices, a lane for each block
+        const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
+        uint32_t n = 0;
+        for (int b = lane; b < a.count_blocks; b += 64) n += part[(size_t)b * row + a.experts + w];
+        n = reduce<64>(n, [](uint32_t p, uint32_t q) { return p + q; });
+        if (lane == 0) work.hist[kCountWords + w] = n;
       }
       __syncthreads();
-      make_share<kBalanceBlock>(a, up, hist, hist[a.experts], share, red);
-    } else {
-      count<kBalanceBlock>(a, i, t0, t1, hist);
-      uint32_t* out = a.part_counts + ((size_t)blockIdx.y * a.blocks + blockIdx.x) * (a.experts + 1);
-      for (int k = threadIdx.x; k < a.experts; k += kBalanceBlock) out[k] = hist[k];
-      if (threadIdx.x == 0) out[a.experts] = hist[kCountWords];
     }
-  }, share, sum, bits);
-  double* out = a.part_probs + ((size_t)blockIdx.y * a.blocks + blockIdx.x) * a.experts;
-  for (int k = threadIdx.x; k < a.experts; k += kBalanceBlock) out[k] = sum[k];
+    if constexpr (MODE != kLossOnly) make_share<kBalanceBlock>(a, up, work.hist, work.share);
+  }, [&](int k, double sum) {
+    out[k] = sum;
+    if constexpr (MODE != kLossOnly) loss += (double)work.hist[k] * sum;
+  }, work);
+  if constexpr (MODE != kLossOnly) {  // this block's tokens' part of the loss
+    loss = wave_sum(loss);
+    if (threadIdx.x % 64 == 0) work.red[threadIdx.x / 64] = loss;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kBalanceBlock / 64; ++w) loss += work.red[w];
+      a.part_loss[(size_t)blockIdx.y * a.loss_parts + blockIdx.x] = loss;
+    }
+  }
 }
 
 // What is left to do for expert k of learner i once its sums are known; returns its part of the
@@ -475,33 +532,26 @@ __device__ __forceinline__ void write_loss(const BalanceArgs& a, int i, uint32_t
 
 template <typename T, int L, int J, bool NARROW, int MODE>
 __global__ __launch_bounds__(kBalanceOne) void k_balance_one(const BalanceArgs a) {
-  __shared__ double sum[kSumWords];
-  __shared__ uint32_t bits[kBlockTokens / 32];
-  __shared__ float share[MODE != kLossOnly ? kMaxExperts : 1];
-  __shared__ uint32_t hist[kCountWords + 1];
-  __shared__ double red[kBalanceOne / 64];
+  __shared__ Work<T, kBalanceOne> work;
   const int i = a.learner[blockIdx.x];
   // read early: nothing of the call's waits for memory after the logits
   const double up = MODE != kLossOnly && a.grad_scale != nullptr ? a.grad_scale[i] : 1.0;
-  int64_t first_total = 0;
-  if (a.totals != nullptr && (int)threadIdx.x < a.experts) first_total = a.totals[(int64_t)i * a.totals_stride + threadIdx.x];
-  const auto total = [&](int k) {
-    return k < kBalanceOne || a.totals == nullptr ? first_total : a.totals[(int64_t)i * a.totals_stride + k];
-  };
+  const int64_t* totals = a.totals != nullptr ? a.totals + (int64_t)i * a.totals_stride : nullptr;
+  const int64_t total = totals != nullptr && (int)threadIdx.x < a.experts ? totals[threadIdx.x] : 0;
+  double loss = 0.0;
   pass<T, L, J, NARROW, MODE, kBalanceOne>(a, i, 0, a.tokens, [&] {
-    count<kBalanceOne>(a, i, 0, a.tokens, hist);
-    if constexpr (MODE != kLossOnly) make_share<kBalanceOne>(a, up, hist, hist[kCountWords], share, red);
-  }, share, sum, bits);
-  const uint32_t kept = hist[kCountWords];
-  double l = 0.0;
-  for (int k = threadIdx.x; k < a.experts; k += kBalanceOne) l += finish_expert(a, i, k, hist[k], sum[k], kept, total(k));
-  l = wave_sum(l);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = l;
+    count<kBalanceOne>(a, i, 0, a.tokens, work.hist);
+    if constexpr (MODE != kLossOnly) make_share<kBalanceOne>(a, up, work.hist, work.share);
+  }, [&](int k, double sum) {
+    const int64_t before = k == (int)threadIdx.x || totals == nullptr ? total : totals[k];
+    loss += finish_expert(a, i, k, work.hist[k], sum, work.hist[kCountWords], before);
+  }, work);
+  loss = wave_sum(loss);
+  if ((threadIdx.x & 63) == 0) work.red[threadIdx.x >> 6] = loss;
   __syncthreads();
   if (threadIdx.x == 0) {
-    l = 0.0;
-    for (int w = 0; w < kBalanceOne / 64; ++w) l += red[w];
-    write_loss(a, i, kept, l);
+    for (int w = 1; w < kBalanceOne / 64; ++w) loss += work.red[w];
+    write_loss(a, i, work.hist[kCountWords], loss);
   }
 }
 

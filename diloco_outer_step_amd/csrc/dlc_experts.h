@@ -12,21 +12,18 @@ namespace dlc {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 64;
-#ifndef VB
-#define VB 256
-#define VA 2
-#define VS 2048
-#endif
-constexpr int kBalanceBlock = VB;       // threads of a block over the logits
-constexpr int kBalanceAhead = VA;
+// Over the logits: blocks of 256 threads with two steps' loads under way behind the one that is worked on.
+// 32768 x 256 x 8 bf16, us a call: 512 threads 82, 256 80 (an early form); one step ahead 73.4, two 72.1 (a
+// later one).
+constexpr int kBalanceBlock = 256;
+constexpr int kBalanceAhead = 2;
 constexpr int kBalanceOne = 512;         // threads of the block that does a learner's whole call
 constexpr int kCountBlock = 512;
 constexpr int kFinalBlock = 512;
-constexpr int kFinalExperts = 32;        // experts of a block of the final sums
+constexpr int kFinalExperts = 32;        // experts of a block of long final sums
 constexpr int kFinalMost = kMaxExperts / kFinalExperts;
 constexpr int kFoldTokens = 16;          // tokens a lane sums in fp32 before it goes on in fp64
 constexpr int kCountWords = 1024;        // LDS words of a block's histogram copies
-constexpr int kSumWords = VS;          // LDS words of the waves' probability sums
 constexpr int kBlockTokens = 16384;      // most tokens of a block over the logits
 constexpr int64_t kCountTokens = 1 << 18;  // most tokens of a counting block, see divide()
 
@@ -46,15 +43,17 @@ struct BalanceArgs {
   float* means;               // [n_learners][experts], or NULL
   int64_t* totals;            // [n_learners][experts], or NULL
   int64_t totals_stride;
-  uint32_t* part_counts;      // [present][count_blocks][experts + 1]: counts, kept tokens
+  uint32_t* part_counts;      // [present][count_blocks][experts + 2]: counts, kept tokens, choices in all
   double* part_probs;         // [present][blocks][experts] sums of probabilities
-  double* part_loss;          // [present][kFinalMost]
+  double* part_loss;          // [present][loss_parts]
   uint32_t* tickets;          // [present]
   double coef;
   int32_t tokens, experts, top;
   uint32_t top_inverse;       // ceil(2^32 / top), 0 for top = 1
   int32_t count_blocks, count_tokens;  // blocks per learner that count, tokens of each
   int32_t blocks, block_tokens;        // blocks per learner over the logits, tokens of each
+  int32_t final_experts;               // of a block of the final sums
+  int32_t loss_parts;
   int32_t accumulate, wide_choices;
   int32_t n_present;
   LearnerList learner;
@@ -81,6 +80,12 @@ inline int balance_lanes(int experts, int v) {
   int l = 1;
   while (l < 64 && l * v < experts) l *= 2;
   return l;
+}
+
+// Tokens of a step of the one block, which has 8 or 64 lanes a token (1 where a row is narrower than a load).
+inline int balance_one_tokens(int32_t type, int experts) {
+  const int v = type == kF32 ? 4 : 8;
+  return kBalanceOne / (experts < v ? 1 : balance_lanes(experts, v) <= 8 ? 8 : 64);
 }
 
 // Kernel launchers (dlc_experts.hip).  Each returns hipSuccess or the launch error.

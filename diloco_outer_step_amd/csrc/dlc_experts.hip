@@ -11,62 +11,72 @@ namespace dlc {
 namespace {
 
 __global__ __launch_bounds__(kCountBlock) void k_balance_count(const BalanceArgs a) {
-  __shared__ uint32_t hist[kCountWords + 1];
+  __shared__ uint32_t hist[kCountWords + 2];
   const int t0 = blockIdx.x * a.count_tokens, t1 = min(a.tokens, t0 + a.count_tokens);
   count<kCountBlock>(a, a.learner[blockIdx.y], t0, t1, hist);
-  uint32_t* out = a.part_counts + ((size_t)blockIdx.y * a.count_blocks + blockIdx.x) * (a.experts + 1);
-  for (int k = threadIdx.x; k < a.experts; k += kCountBlock) out[k] = hist[k];
-  if (threadIdx.x == 0) out[a.experts] = hist[kCountWords];
+  write_counts<kCountBlock>(a, a.part_counts + ((size_t)blockIdx.y * a.count_blocks + blockIdx.x) * (a.experts + 2), hist);
 }
 
-// A block per kFinalExperts experts of a learner: thread (s, k) sums every kFinalSlices-th
-// block's expert k, then the slices in order.  One block would do, but it is a single CU's
-// outstanding loads that limit it (131 KB of sums: 8 us).  The block that comes last,
-// which a ticket tells it, adds the blocks' parts of the loss, in their order.
+// A block per a.final_experts experts of a learner (a power of two): thread (s, c) sums every slices-th
+// block's expert c, then the slices in order.  One block for all experts is limited by a single
+// CU's outstanding loads (131 KB of sums: 8 us against 5), so long sums are split by
+// experts.  The loss is a sum over all of them.  With a gradient the blocks over the logits knew the
+// counts and left their tokens' parts of it, which the first block adds; without one the block
+// that comes last, which a ticket tells it, adds the blocks' parts, in their order.
 __global__ __launch_bounds__(kFinalBlock) void k_balance_final(const BalanceArgs a) {
-  constexpr int kSlices = kFinalBlock / kFinalExperts;
   __shared__ double sums[kFinalBlock];
   __shared__ uint32_t counts[kFinalBlock];
   __shared__ uint32_t kept_part[kFinalBlock / 64];
-  const int e = a.experts, s = threadIdx.x / kFinalExperts, c = threadIdx.x % kFinalExperts;
-  const int k = blockIdx.x * kFinalExperts + c, i = a.learner[blockIdx.y];
+  __shared__ double red[kFinalBlock / 64];
+  const int e = a.experts, width = a.final_experts, slices = kFinalBlock / width;
+  const int s = threadIdx.x / width, c = threadIdx.x % width;
+  const int k = blockIdx.x * width + c, i = a.learner[blockIdx.y];
   const bool mine = k < e;
-  const uint32_t* part = a.part_counts + (size_t)blockIdx.y * a.count_blocks * (e + 1);
+  const uint32_t* part = a.part_counts + (size_t)blockIdx.y * a.count_blocks * (e + 2);
   const double* prob = a.part_probs + (size_t)blockIdx.y * a.blocks * e + (mine ? k : 0);
   const int64_t total = a.totals != nullptr && mine && s == 0 ? a.totals[(int64_t)i * a.totals_stride + k] : 0;
   uint32_t n = 0, count = 0;
-  for (int b = threadIdx.x; b < a.count_blocks; b += kFinalBlock) n += part[(size_t)b * (e + 1) + e];
+  for (int b = threadIdx.x; b < a.count_blocks; b += kFinalBlock) n += part[(size_t)b * (e + 2) + e];
 #pragma unroll 4
-  for (int b = s; b < a.count_blocks; b += kSlices) count += part[(size_t)b * (e + 1) + (mine ? k : 0)];
+  for (int b = s; b < a.count_blocks; b += slices) count += part[(size_t)b * (e + 2) + (mine ? k : 0)];
+  const bool parts = a.grad != nullptr;
+  double l = 0.0;
+  if (parts && blockIdx.x == 0) {
+    for (int b = threadIdx.x; b < a.blocks; b += kFinalBlock) l += a.part_loss[(size_t)blockIdx.y * a.loss_parts + b];
+  }
   double v = 0.0;
 #pragma unroll 8
-  for (int b = s; b < a.blocks; b += kSlices) v += prob[(size_t)b * e];
+  for (int b = s; b < a.blocks; b += slices) v += prob[(size_t)b * e];
   sums[threadIdx.x] = v;
   counts[threadIdx.x] = count;
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) n += __shfl_xor(n, m, 64);
   if ((threadIdx.x & 63) == 0) kept_part[threadIdx.x >> 6] = n;
   __syncthreads();
-  if (threadIdx.x >= 64) return;
   uint32_t kept = 0;
 #pragma unroll
   for (int w = 0; w < kFinalBlock / 64; ++w) kept += kept_part[w];
-  double l = 0.0;
   if (s == 0 && mine) {
-#pragma unroll
-    for (int q = 1; q < kSlices; ++q) {
-      v += sums[q * kFinalExperts + c];
-      count += counts[q * kFinalExperts + c];
+#pragma unroll 4
+    for (int q = 1; q < slices; ++q) {
+      v += sums[q * width + c];
+      count += counts[q * width + c];
     }
-    l = finish_expert(a, i, k, count, v, kept, total);
+    const double part = finish_expert(a, i, k, count, v, kept, total);
+    if (!parts) l = part;
   }
+  if (parts && blockIdx.x != 0) return;
   l = wave_sum(l);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = l;
+  __syncthreads();
   if (threadIdx.x != 0) return;
-  if (gridDim.x == 1) {
+  for (int w = 1; w < kFinalBlock / 64; ++w) l += red[w];
+  if (parts) l = kept == 0 ? 0.0 : l / (double)kept;
+  if (parts || gridDim.x == 1) {
     write_loss(a, i, kept, l);
     return;
   }
-  double* losses = a.part_loss + (size_t)blockIdx.y * kFinalMost;
+  double* losses = a.part_loss + (size_t)blockIdx.y * a.loss_parts;
   __hip_atomic_store(&losses[blockIdx.x], l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   const uint32_t drawn = __hip_atomic_fetch_add(&a.tickets[blockIdx.y], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
   if (drawn != gridDim.x - 1) return;
@@ -109,7 +119,7 @@ hipError_t launch_balance_count(const BalanceArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_balance_final(const BalanceArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(k_balance_final, dim3((a.experts + kFinalExperts - 1) / kFinalExperts, a.n_present),
+  hipLaunchKernelGGL(k_balance_final, dim3((a.experts + a.final_experts - 1) / a.final_experts, a.n_present),
                      dim3(kFinalBlock), 0, s, a);
   return hipGetLastError();
 }

@@ -24,25 +24,37 @@ using dlc::round256;
 static_assert(dlc::kMaxExperts == DLC_MAX_EXPERTS && dlc::kMaxChoices == DLC_MAX_CHOICES);
 static_assert((dlc::kCountTokens - 1) * (int64_t)DLC_MAX_CHOICES * (DLC_MAX_CHOICES - 1) < (int64_t(1) << 32));
 
-#ifndef VN
-#define VN 1024
-#define VM 2
-#define VC 4096
-#endif
-constexpr int64_t kBalanceBlocks = VN;   // over the logits, all learners
-constexpr int64_t kMinSteps = VM;           // of a block over the logits
-constexpr int64_t kCountChoices = VC;    // choices of a counting block
+// Blocks over the logits, all learners: four for each CU, so all of them run at once and what a block
+// does before and after its tokens (2 us) is done once.  1024, 1280 blocks: 32768 x 256 x 8 bf16 with the gradient
+// 63.8, 65.5 us, 16384 x 128 x 8 without 17.8, 19.7 us (2048: 23.8 against 19.7 of an earlier form).
+constexpr int64_t kBalanceBlocks = 1024;
+constexpr int64_t kMinSteps = 2;           // of a block over the logits (1 or 2 are the same within 2%)
+// Choices of a counting block: one load of 8 for each of its 512 threads (2048 and 8192 are within 1 us).
+constexpr int64_t kCountChoices = 4096;
 constexpr int64_t kMaxCountBlocks = 32;    // per learner, as long as a block's tokens stay below kCountTokens
+// Up to so many choices every block counts all of its learner's for itself, which saves the counting kernel: four
+// rounds of 8 loads a thread, which take no longer (and eagerly 3 us less).  With 20000 choices it is 26 us a
+// call against 16.
+constexpr int64_t kSelfCount = 8192;
+// Up to so many sums (blocks times experts) one block a learner does the final ones: above it a single CU's
+// loads take longer than the ticket of several blocks (16384 sums: 20.4 us a call against 18.5).
+constexpr int64_t kOneFinal = 8192;
 constexpr int64_t kMaxStride = int64_t(1) << 48;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Calls this small run in one block per learner.
-constexpr int64_t kOneLogits = 16384, kOneChoices = 16384;
+// Calls of so few steps run in one block per learner.  One block against the passes over the logits and the
+// final sums (us a call replayed from a graph, eight learners, bf16 / eagerly, one learner):
+//   64 experts    128 tokens: 6.5, 9.8 / 9.2, 12.7   512: 9.2, 9.8 / 9.3, 12.8   1024: 12.9, 11.1 / 12.6, 12.5
+//   256 experts    32 tokens: 7.5, 9.7 / 9.1, 12.5    64: 10.0, 10.0 / 9.9, 12.6   128: 14.9, 10.4 / 14.4, 12.6
+//   8 experts     256 tokens: 7.8, 10.0 / 9.6, 12.9  1024: 13.3, 10.5 / 13.1, 12.7
+// a step being 64, 8 and 64 tokens.
+constexpr int64_t kOneSteps = 8;
+constexpr int64_t kOneChoices = 8192;
 
-bool one_block(int64_t tokens, int64_t experts, int64_t top) {
-  static_assert(kOneLogits <= dlc::kBlockTokens);
-  return tokens * experts <= kOneLogits && tokens * top <= kOneChoices;
+bool one_block(int64_t tokens, int32_t experts, int64_t top, int32_t type) {
+  static_assert(kOneSteps * dlc::kBalanceOne <= dlc::kBlockTokens);
+  return tokens <= kOneSteps * dlc::balance_one_tokens(type, experts) && tokens * top <= kOneChoices;
 }
 
 struct BalancePartition {
@@ -60,7 +72,7 @@ BalancePartition balance_partition(int64_t tokens, int32_t experts, int64_t top,
   p.count_blocks = p.blocks;
   p.count_tokens = p.block_tokens;
   if (gradient) {
-    const int64_t want = std::min(kMaxCountBlocks, std::max<int64_t>(1, ceil_div(tokens * top, kCountChoices)));
+    const int64_t want = tokens * top <= kSelfCount ? 1 : std::min(kMaxCountBlocks, ceil_div(tokens * top, kCountChoices));
     p.count_tokens = std::min(std::max<int64_t>(1, ceil_div(tokens, want)), dlc::kCountTokens);
     p.count_blocks = std::max<int64_t>(1, ceil_div(tokens, p.count_tokens));
   }
@@ -72,11 +84,14 @@ size_t probs_bytes(const BalancePartition& p, int32_t experts, int32_t present) 
 }
 
 size_t counts_bytes(const BalancePartition& p, int32_t experts, int32_t present) {
-  return round256((size_t)present * p.count_blocks * (experts + 1) * sizeof(uint32_t));
+  return round256((size_t)present * p.count_blocks * (experts + 2) * sizeof(uint32_t));
 }
 
-size_t loss_bytes(int32_t present) {
-  return round256((size_t)present * (dlc::kFinalMost * sizeof(double) + sizeof(uint32_t)));
+// the blocks' parts of the loss (over the logits, or of the final sums), and a ticket
+int64_t loss_parts(const BalancePartition& p) { return std::max<int64_t>(p.blocks, dlc::kFinalMost); }
+
+size_t loss_bytes(const BalancePartition& p, int32_t present) {
+  return round256((size_t)present * (loss_parts(p) * sizeof(double) + sizeof(uint32_t)));
 }
 
 int32_t check_sizes(int32_t n_learners, int64_t n_tokens, int32_t n_experts) {
@@ -125,7 +140,7 @@ int32_t dlc_expert_balance_workspace_bytes(int32_t n_learners, int64_t n_tokens,
       for (const int32_t type : {DLC_FLOAT32, DLC_BFLOAT16}) {
         for (const bool gradient : {false, true}) {
           const BalancePartition p = balance_partition(n_tokens, n_experts, DLC_MAX_CHOICES, type, present, gradient);
-          most = std::max(most, probs_bytes(p, n_experts, present) + counts_bytes(p, n_experts, present) + loss_bytes(present));
+          most = std::max(most, probs_bytes(p, n_experts, present) + counts_bytes(p, n_experts, present) + loss_bytes(p, present));
         }
       }
     }
@@ -186,12 +201,12 @@ int32_t dlc_expert_balance(const void* logits, int32_t logits_type, int64_t logi
         (several && totals && totals_stride < n_experts))
       return fail(DLC_ERR_INVALID_ARGUMENT, "rows of counts or totals overlap");
     const bool gradient = grad_logits != nullptr && n_tokens > 0;
-    const bool one = one_block(n_tokens, n_experts, n_choices);
+    const bool one = one_block(n_tokens, n_experts, n_choices, logits_type);
     const BalancePartition p =
         balance_partition(n_tokens, n_experts, n_choices, logits_type, a.n_present, gradient);
     const size_t probs = probs_bytes(p, n_experts, a.n_present);
     const size_t losses = probs + counts_bytes(p, n_experts, a.n_present);
-    const size_t need = one ? 0 : losses + loss_bytes(a.n_present);
+    const size_t need = one ? 0 : losses + loss_bytes(p, a.n_present);
     if (workspace == nullptr || workspace_bytes < need)
       return fail(DLC_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
     if (!aligned256(workspace)) return fail(DLC_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
@@ -231,7 +246,7 @@ int32_t dlc_expert_balance(const void* logits, int32_t logits_type, int64_t logi
     a.part_probs = static_cast<double*>(workspace);
     a.part_counts = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + probs);
     a.part_loss = reinterpret_cast<double*>(static_cast<char*>(workspace) + losses);
-    a.tickets = reinterpret_cast<uint32_t*>(a.part_loss + (size_t)a.n_present * dlc::kFinalMost);
+    a.tickets = reinterpret_cast<uint32_t*>(a.part_loss + (size_t)a.n_present * loss_parts(p));
     a.coef = coef;
     a.tokens = (int32_t)n_tokens;
     a.experts = n_experts;
@@ -240,13 +255,18 @@ int32_t dlc_expert_balance(const void* logits, int32_t logits_type, int64_t logi
     a.count_blocks = (int32_t)p.count_blocks;
     a.count_tokens = (int32_t)p.count_tokens;
     a.blocks = (int32_t)p.blocks;
+    a.loss_parts = (int32_t)loss_parts(p);
+    a.final_experts = dlc::kFinalExperts;
+    if (p.blocks * n_experts <= kOneFinal) {
+      while (a.final_experts < std::min(n_experts, dlc::kFinalBlock)) a.final_experts *= 2;
+    }
     a.block_tokens = (int32_t)p.block_tokens;
     const hipStream_t st = static_cast<hipStream_t>(hip_stream);
     hipError_t e;
     if (one) {
       e = dlc::launch_balance(a, logits_type, true, st);
     } else {
-      e = gradient ? dlc::launch_balance_count(a, st) : hipSuccess;
+      e = gradient && p.count_blocks > 1 ? dlc::launch_balance_count(a, st) : hipSuccess;
       if (e == hipSuccess) e = dlc::launch_balance(a, logits_type, false, st);
       if (e == hipSuccess) e = dlc::launch_balance_final(a, st);
     }
