@@ -125,7 +125,12 @@ constexpr int64_t kMergeTilesPerBlock = 2;
 // each block first builds its K scaled codebook tables: it does best with
 // coarser blocks than the merge.
 constexpr int64_t kDirectionBlocks = 16384;
+constexpr int64_t kSquaresBlocks = 16384;
 constexpr int64_t kBroadcastBlocks = 8192;
+// The merged gradient's norm over so few tiles runs in one block (four tiles at a time, one launch
+// instead of two) as long as its tables fit in LDS.
+constexpr int64_t kOneNormTiles = 8;
+constexpr int32_t kOneNormLearners = 16;
 // At least one full group of 4 tiles per statistics or encode block: on a
 // single 4096^2 tensor, 4-tile blocks ran the step 27% faster than 1-tile blocks
 // (per-block setup, histogram flush and pipeline start amortized); large sets
@@ -205,6 +210,11 @@ Partition broadcast_partition(const dlc_tensor* t, int32_t n) {
 
 Partition direction_partition(const dlc_tensor* t, int32_t n) {
   return make_partition(t, n, kUnlimitedTiles, kDirectionBlocks / dlc::kMergeTiles, dlc::kMergeTiles);
+}
+
+// The merged gradient's squares: as the direction pass, blocks that first build their tables.
+Partition squares_partition(const dlc_tensor* t, int32_t n) {
+  return make_partition(t, n, kUnlimitedTiles, kSquaresBlocks);
 }
 
 // merge blocks work on kMergeTiles tiles side by side, kMergeTilesPerBlock in all
@@ -1250,7 +1260,7 @@ int32_t dlc_outer_grad_norm_workspace_bytes(const dlc_tensor* tensors, int32_t n
     if (!bytes) return fail(DLC_ERR_INVALID_ARGUMENT, "bytes is NULL");
     const int32_t rc = check_tensors(tensors, n_tensors, 0, false);
     if (rc != DLC_OK) return rc;
-    *bytes = round256((size_t)direction_partition(tensors, n_tensors).n_slots * sizeof(double));
+    *bytes = round256((size_t)squares_partition(tensors, n_tensors).n_slots * sizeof(double));
     return ok();
   });
 }
@@ -1273,7 +1283,7 @@ int32_t dlc_outer_grad_norm(const uint8_t* codes, int64_t learner_stride, int32_
     int32_t rc = merge_weights(a, weights, n_learners);
     if (rc == DLC_OK) rc = check_tensors(tensors, n_tensors, learner_stride, true);
     if (rc != DLC_OK) return rc;
-    const Partition p = direction_partition(tensors, n_tensors);
+    const Partition p = squares_partition(tensors, n_tensors);
     const size_t need = round256((size_t)p.n_slots * sizeof(double));
     if (workspace == nullptr || workspace_bytes < need)
       return fail(DLC_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
@@ -1289,11 +1299,17 @@ int32_t dlc_outer_grad_norm(const uint8_t* codes, int64_t learner_stride, int32_
     a.tensor_w = tensor_weights;
     a.dir_part = static_cast<double*>(workspace);
     const hipStream_t st = static_cast<hipStream_t>(hip_stream);
+    const dlc::OuterNormArgs out{a.dir_part, norm, grad_scale, max_norm, p.n_slots};
+    // few tiles are one to a block in this partition
+    if (p.n_slots <= kOneNormTiles && a.n_present <= kOneNormLearners && p.launches[0].tiles_per_block == 1) {
+      const hipError_t e = dlc::launch_outer_norm_one(a, p.launches[0], out, st);
+      return e != hipSuccess ? hip_fail(e, "outer gradient norm kernel launch") : ok();
+    }
     for (const dlc::LaunchGeom& g : p.launches) {
       const hipError_t e = dlc::launch_outer_squares(a, g, st);
       if (e != hipSuccess) return hip_fail(e, "outer gradient kernel launch");
     }
-    const hipError_t e = dlc::launch_outer_norm({a.dir_part, norm, grad_scale, max_norm, p.n_slots}, st);
+    const hipError_t e = dlc::launch_outer_norm(out, st);
     return e != hipSuccess ? hip_fail(e, "outer gradient norm kernel launch") : ok();
   });
 }

@@ -142,6 +142,8 @@ struct RingArgs {
   int32_t cb_row[kMaxTensorsPerLaunch];  // codebook row of the message each segment of the launch receives
 };
 
+static_assert(sizeof(MergeArgs) + sizeof(LaunchGeom) + sizeof(OuterNormArgs) <= 4096);
+
 // Kernel launchers (dlc_kernels.hip).  Each returns hipSuccess or the launch error.
 hipError_t launch_stats(const QuantArgs& a, const LaunchGeom& g, hipStream_t s);
 hipError_t launch_range(const QuantArgs& a, const LaunchGeom& g, hipStream_t s);
@@ -158,6 +160,8 @@ hipError_t launch_rda_coef(const MergeArgs& a, const LaunchGeom& g, hipStream_t 
 // The merged gradient's norm: sums of squares per block (dir_part), then norm and factor
 hipError_t launch_outer_squares(const MergeArgs& a, const LaunchGeom& g, hipStream_t s);
 hipError_t launch_outer_norm(const OuterNormArgs& a, hipStream_t s);
+// the same in one kernel of one block; g has one tile a block, and few
+hipError_t launch_outer_norm_one(const MergeArgs& a, const LaunchGeom& g, const OuterNormArgs& out, hipStream_t s);
 hipError_t launch_broadcast(const BroadcastArgs& a, const LaunchGeom& g, hipStream_t s);
 // segments: (offset of the chunk in theta_g, the receiver's offset in the flat theta_L / accum,
 // numel); the sender's codes sit one rank row earlier, cyclically; the launch geometry must be the

@@ -40,6 +40,7 @@
 // (checked against the exact division near bucket edges) and the fixed-point
 // histogram position.
 #include "dlc_internal.h"
+#include "dlc_lanes.h"
 
 #include <cfloat>
 #include <type_traits>
@@ -94,8 +95,12 @@ __device__ __forceinline__ int f4_index(int tid, int j) { return (tid & ~63) * 4
 // instruction, so ring slots without data keep the wait counts static.
 constexpr int kBufferWord3 = 0x00020000;
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const float* p, int elems) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), (short)0, elems * 4, kBufferWord3);
+}
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const float* p, bool valid) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), (short)0, valid ? kTile * 4 : 0, kBufferWord3);
+  return tile_rsrc(p, valid ? kTile : 0);
 }
 
 __device__ __forceinline__ void load_tile_rsrc(__amdgpu_buffer_rsrc_t r, int tid, float (&v)[kVec]) {
@@ -791,27 +796,28 @@ __global__ __launch_bounds__(kBuckets) void k_codebook(const QuantArgs a, const 
 // k_merge: g = sum_i tab_i[code_i] with tab_i[c] = w_hat_i * codebook_i[c] (fp64,
 // in LDS), learners in index order; then the Nesterov step in fp64.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void nesterov1(float& t, float& v, double g, double lr, double beta) {
+  const double bv = beta * (double)v;
+  const double vn = bv + g;
+  const double bvn = beta * vn;
+  const double step = g + bvn;
+  const double u = lr * step;
+  const double tn = (double)t - u;
+  t = (float)tn;
+  v = (float)vn;
+}
+
 __device__ __forceinline__ void nesterov16(float (&tv)[kVec], float (&vv)[kVec], const double (&acc)[kVec],
                                            double lr, double beta) {
 #pragma unroll
-  for (int e = 0; e < kVec; ++e) {
-    const double gsum = acc[e];
-    const double bv = beta * (double)vv[e];
-    const double vn = bv + gsum;
-    const double bvn = beta * vn;
-    const double step = gsum + bvn;
-    const double u = lr * step;
-    const double tn = (double)tv[e] - u;
-    tv[e] = (float)tn;
-    vv[e] = (float)vn;
-  }
+  for (int e = 0; e < kVec; ++e) nesterov1(tv[e], vv[e], acc[e], lr, beta);
 }
 
 // Code words of one (learner, tile) item: 4 dwords per lane through a buffer
-// descriptor covering the tile's 4096 codes (zero records = null request).
-__device__ __forceinline__ void load_codes_rsrc(const uint8_t* cp, bool valid, int tid, uint32_t (&cw)[4]) {
+// descriptor covering the tile's codes (zero records = null request).
+__device__ __forceinline__ void load_codes_rsrc(const uint8_t* cp, int elems, int tid, uint32_t (&cw)[4]) {
   const __amdgpu_buffer_rsrc_t r =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(cp), (short)0, valid ? kTile : 0, kBufferWord3);
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(cp), (short)0, elems, kBufferWord3);
 #pragma unroll
   for (int j = 0; j < 4; ++j) cw[j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, f4_index(tid, j) * 4, 0, 2);
 }
@@ -833,7 +839,7 @@ __device__ __forceinline__ void store_tile_rsrc(__amdgpu_buffer_rsrc_t r, int ti
 // A merge block is kMergeTiles groups of kBlock threads; group q works on tile
 // kMergeTiles * s + q of the block's span in round s, so every learner's codes,
 // theta and momentum move in runs of kMergeTiles * 4 KB (codes) and
-// kMergeTiles * 16 KB per block.  Tiles past the block's full tiles are null
+// kMergeTiles * 16 KB per block.  Tiles past the block's are null
 // requests and dropped stores (wave-uniform: a group is 4 whole waves).
 // Code words of (learner, round) items stream through a ring of kMergeRing
 // registers (item i + kMergeRing - 1 is requested while item i is looked up),
@@ -866,8 +872,7 @@ __device__ __forceinline__ double rda_unit_weight(const MergeArgs& a, const Laun
 }
 
 //
-// The clipped step's table holds scale * w * codebook_i[c] with the tensor's own weights
-// w, and DIR without norm2 sums the squares of the merged gradient with them.
+// The clipped step's table holds scale * w * codebook_i[c] with the tensor's own weights w.
 __device__ __forceinline__ double merge_weight(const MergeArgs& a, size_t trow, int k) {
   return a.tensor_w != nullptr ? a.tensor_w[trow * a.n_learners + a.learner[k]] : a.w_hat[k];
 }
@@ -891,7 +896,7 @@ __global__ __launch_bounds__(kMergeBlock) __attribute__((amdgpu_waves_per_eu(4))
     const int k = i >> 8, c = i & (kBuckets - 1);
     const float cb = a.codebook[((size_t)a.learner[k] * g.n_tensors_call + trow) * kBuckets + c];
     double w;
-    if (DIR) w = a.norm2 != nullptr ? rda_unit_weight(a, g, trow, k) : merge_weight(a, trow, k);
+    if (DIR) w = rda_unit_weight(a, g, trow, k);
     else w = a.coef != nullptr ? a.coef[trow * kp + k] : scale * merge_weight(a, trow, k);
     tab[i] = w != 0.0 ? w * (double)cb : 0.0;  // a weight of 0 leaves the learner out, whatever its codebook holds
   }
@@ -903,110 +908,88 @@ __global__ __launch_bounds__(kMergeBlock) __attribute__((amdgpu_waves_per_eu(4))
   auto codes_of = [&](int k) { return a.codes + (int64_t)a.learner[k] * a.stride + td.loffset(); };
   const double lr = a.lr, beta = a.beta;
 
-  const int64_t n_full = (sp.end - sp.begin) / kTile;
-  if (n_full > 0) {
-    const int items = NR > 0 ? NR * kMergeRing : (kp + kMergeRing - 1) / kMergeRing * kMergeRing;
-    const int64_t n_rounds = (n_full + kMergeTiles - 1) / kMergeTiles;
-    // this group's tile of round r (element offset in the tensor) and whether it is full
-    auto tile_of = [&](int64_t r) { return r * kMergeTiles + q; };
-    auto request = [&](uint32_t (&dst)[4], int64_t r, int i) {
-      const int64_t tile = tile_of(r);
-      const bool valid = i < kp && tile < n_full;
-      load_codes_rsrc(codes_of(i < kp ? i : kp - 1) + sp.begin + (valid ? tile : 0) * kTile, valid, tid, dst);
-    };
-    uint32_t ring[kMergeRing][4];
+  // The tensor's last tile may be partial.  The descriptors of its theta and momentum end with its last whole group
+  // of 4 elements, so that every access lies within them or without; up to 3 elements are left to the end.  Those of
+  // the codes end with the last group that holds any (a row's tensors own whole groups of 64).
+  const int64_t n_tiles = (sp.end - sp.begin + kTile - 1) / kTile;
+  const int rest = DIR ? 0 : (int)((sp.end - sp.begin) & 3);
+  auto tile_elems = [&](int64_t tile) {
+    const int64_t n = sp.end - sp.begin - tile * kTile;
+    return n < kTile ? (int)n : kTile;
+  };
+  const int items = NR > 0 ? NR * kMergeRing : (kp + kMergeRing - 1) / kMergeRing * kMergeRing;
+  const int64_t n_rounds = (n_tiles + kMergeTiles - 1) / kMergeTiles;
+  // this group's tile of round r (element offset in the tensor) and whether there is one
+  auto tile_of = [&](int64_t r) { return r * kMergeTiles + q; };
+  auto request = [&](uint32_t (&dst)[4], int64_t r, int i) {
+    const int64_t tile = tile_of(r);
+    const bool valid = i < kp && tile < n_tiles;
+    load_codes_rsrc(codes_of(i < kp ? i : kp - 1) + sp.begin + (valid ? tile : 0) * kTile,
+                    valid ? (tile_elems(tile) + 3) & ~3 : 0, tid, dst);
+  };
+  uint32_t ring[kMergeRing][4];
 #pragma unroll
-    for (int i = 0; i < kMergeRing - 1; ++i) request(ring[i], 0, i);
-    if (NR > 0 && !DIR) {
-      const __amdgpu_buffer_rsrc_t none = __builtin_amdgcn_make_buffer_rsrc(th, (short)0, 0, kBufferWord3);
-      const float zero[kVec] = {};
-      store_tile_rsrc(none, tid, zero);
-      store_tile_rsrc(none, tid, zero);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    for (int64_t r = 0; r < n_rounds; ++r) {
-      const int64_t tile = tile_of(r);
-      const bool valid = tile < n_full;
-      const int64_t base = sp.begin + (valid ? tile : 0) * kTile;
-      const __amdgpu_buffer_rsrc_t rt = tile_rsrc(th + base, valid && !DIR), rv = tile_rsrc(mv + base, valid && !DIR);
-      float tv[kVec], vv[kVec];
-      if (!DIR) {
-        load_tile_rsrc(rt, tid, tv);
-        load_tile_rsrc(rv, tid, vv);
-      }
-      double acc[kVec];
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) acc[e] = 0.0;
-      constexpr int kRoundsUnroll = NR > 0 ? NR : 1;
-#pragma unroll kRoundsUnroll
-      for (int i0 = 0; i0 < items; i0 += kMergeRing) {
-#pragma unroll
-        for (int u = 0; u < kMergeRing; ++u) {
-          const int i = i0 + u;
-          const int ip = i + kMergeRing - 1;
-          if (ip < items) request(ring[(u + kMergeRing - 1) % kMergeRing], r, ip);
-          else request(ring[(u + kMergeRing - 1) % kMergeRing], r + 1, ip - items);
-          if (i < kp) {
-            const double* tk = tab + i * kBuckets;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) acc[4 * j + c] += tk[(ring[u][j] >> (8 * c)) & 0xffu];
-            }
-          }
-        }
-      }
-      if (DIR) {
-        if (valid) {
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) dsum += acc[e] * acc[e];
-        }
-      } else {
-        nesterov16(tv, vv, acc, lr, beta);
-        store_tile_rsrc(rt, tid, tv);
-        store_tile_rsrc(rv, tid, vv);
-      }
-    }
+  for (int i = 0; i < kMergeRing - 1; ++i) request(ring[i], 0, i);
+  if (NR > 0 && !DIR) {
+    const __amdgpu_buffer_rsrc_t none = __builtin_amdgcn_make_buffer_rsrc(th, (short)0, 0, kBufferWord3);
+    const float zero[kVec] = {};
+    store_tile_rsrc(none, tid, zero);
+    store_tile_rsrc(none, tid, zero);
   }
-  const int64_t full_end = sp.begin + n_full * kTile;
-  if (q == 0 && full_end < sp.end) {
-    const int64_t n = sp.end - full_end;
+  __builtin_amdgcn_sched_barrier(0);
+  for (int64_t r = 0; r < n_rounds; ++r) {
+    const int64_t tile = tile_of(r);
+    const bool valid = tile < n_tiles;
+    const int64_t base = sp.begin + (valid ? tile : 0) * kTile;
+    const int elems = valid ? tile_elems(tile) : 0;
+    const int whole = DIR ? 0 : elems & ~3;
+    const __amdgpu_buffer_rsrc_t rt = tile_rsrc(th + base, whole), rv = tile_rsrc(mv + base, whole);
     float tv[kVec], vv[kVec];
     if (!DIR) {
-      load_tail(th + full_end, tid, n, tv);
-      load_tail(mv + full_end, tid, n, vv);
+      load_tile_rsrc(rt, tid, tv);
+      load_tile_rsrc(rv, tid, vv);
     }
     double acc[kVec];
 #pragma unroll
     for (int e = 0; e < kVec; ++e) acc[e] = 0.0;
-    for (int k = 0; k < kp; ++k) {
-      const uint8_t* cp = codes_of(k) + full_end;
-      const double* tk = tab + k * kBuckets;
+    constexpr int kRoundsUnroll = NR > 0 ? NR : 1;
+#pragma unroll kRoundsUnroll
+    for (int i0 = 0; i0 < items; i0 += kMergeRing) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int u = 0; u < kMergeRing; ++u) {
+        const int i = i0 + u;
+        const int ip = i + kMergeRing - 1;
+        if (ip < items) request(ring[(u + kMergeRing - 1) % kMergeRing], r, ip);
+        else request(ring[(u + kMergeRing - 1) % kMergeRing], r + 1, ip - items);
+        if (i < kp) {
+          const double* tk = tab + i * kBuckets;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (tail_valid(tid, j, c, n)) acc[4 * j + c] += tk[cp[elem_index(tid, j, c)]];
-        }
-      }
-    }
-    if (DIR) {
+          for (int j = 0; j < 4; ++j) {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) dsum += acc[e] * acc[e];  // invalid elements hold 0
-    } else {
-      nesterov16(tv, vv, acc, lr, beta);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (tail_valid(tid, j, c, n)) {
-            const int64_t e = full_end + elem_index(tid, j, c);
-            th[e] = tv[4 * j + c];
-            mv[e] = vv[4 * j + c];
+            for (int c = 0; c < 4; ++c) acc[4 * j + c] += tk[(ring[u][j] >> (8 * c)) & 0xffu];
           }
         }
       }
     }
+    if (DIR) {
+      if (elems < kTile) {  // what lies outside the tile counts for nothing
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] = elem_index(tid, e / 4, e % 4) < elems ? acc[e] : 0.0;
+      }
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) dsum += acc[e] * acc[e];
+    } else {
+      nesterov16(tv, vv, acc, lr, beta);
+      store_tile_rsrc(rt, tid, tv);
+      store_tile_rsrc(rv, tid, vv);
+    }
+  }
+  // the last up to 3 elements of a tensor whose size is no multiple of 4
+  if (rest != 0 && (int)threadIdx.x < rest) {
+    const int64_t e = sp.end - rest + threadIdx.x;
+    double gsum = 0.0;
+    for (int k = 0; k < kp; ++k) gsum += tab[k * kBuckets + codes_of(k)[e]];
+    nesterov1(th[e], mv[e], gsum, lr, beta);
   }
   if (DIR) {
     __shared__ double red[kMergeBlock / 64];
@@ -1054,12 +1037,156 @@ __global__ __launch_bounds__(kBuckets) void k_rda_coef(const MergeArgs a, const 
   for (int k = threadIdx.x; k < kp; k += kBuckets) a.coef[trow * kp + k] = scale * rda_unit_weight(a, g, trow, k);
 }
 
+// ---------------------------------------------------------------------------
+// k_outer_squares: the sum of squares of the merged gradient per block, from the codes alone
+// (K bytes a parameter).
+//
+// What bounds it is LDS: one lookup for each code.  fp64 tables take 4.75 clocks a wave's lookup (two passes
+// of 32 lanes, and conflicts: 98% of the kernel's time), 32-bit ones about 3.5.  So an entry is a
+// 32-bit integer, round(w_i cb_i[c] / unit), unit = M / (2^31 - 64), M = sum_i |w_i| max_c |cb_i[c]|:
+// no sum over the learners can overflow, integers add in one instruction and without error, and
+// g is off by at most K / 2 units, K 2^-32 of M: 2^-26 of it at the most that a call takes, where an
+// fp32 entry would be off by 2^-24 of itself.  Squares are summed in fp64.  An entry that is not
+// finite, whether a code refers to it or not, makes the sum NaN.
+//
+// A thread holds 16 consecutive codes of every learner (16-byte loads).  Up to 8 learners: a learner's
+// codes of the next tile are requested as soon as its codes of this one are looked up, so
+// K KB a wave are always under way.  More learners take rounds of 8, padded with null requests.
+// ---------------------------------------------------------------------------
+constexpr int kSquaresRing = 8;
+constexpr int kSquaresRounds = kMaxLearners / kSquaresRing;
+
+struct SquaresLds {
+  float largest[kWaves][kMaxLearners];
+  double weight[kMaxLearners];
+  double unit, inverse;
+  double red[kWaves];
+};
+
+// RING learners a round, ROUNDS rounds a tile.
+template <int RING, int ROUNDS>
+__global__ __launch_bounds__(kBlock) void k_outer_squares(const MergeArgs a, const LaunchGeom g) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  int* tab = reinterpret_cast<int*>(smem);
+  SquaresLds& lds = *reinterpret_cast<SquaresLds*>(smem + (size_t)a.n_present * kBuckets * sizeof(int));
+  const int kp = a.n_present, tid = threadIdx.x;
+  const Span sp = block_span(g);
+  const TensorDesc td = g.t[sp.t];
+  const size_t trow = (size_t)g.row_base + g.t_base + sp.t;
+  const int64_t n_tiles = (sp.end - sp.begin + kTile - 1) / kTile;
+  // codes of (tile, learner), 16 for each thread: what lies behind the tensor in its last group of 64 is read too
+  const auto request = [&](vu4& dst, int64_t tile, int k) {
+    const bool valid = k < kp && tile < n_tiles;
+    const int64_t from = sp.begin + (valid ? tile : 0) * kTile;
+    const uint8_t* p = a.codes + (int64_t)a.learner[k < kp ? k : kp - 1] * a.stride + td.loffset() + from;
+    const int64_t left = (sp.end - from + 63) & ~(int64_t)63;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(p), (short)0, valid ? (int)(left < kTile ? left : kTile) : 0, kBufferWord3);
+    dst = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, tid * 16, 0, 2));
+  };
+  vu4 ring[RING];
+#pragma unroll
+  for (int u = 0; u < RING; ++u) request(ring[u], 0, u);
+
+  float* cb = reinterpret_cast<float*>(tab);
+  for (int k0 = 0; k0 < kp; k0 += RING) {
+    float c[RING];
+#pragma unroll
+    for (int u = 0; u < RING; ++u) {
+      const int k = k0 + u < kp ? k0 + u : kp - 1;
+      c[u] = a.codebook[((size_t)a.learner[k] * g.n_tensors_call + trow) * kBuckets + tid];
+    }
+#pragma unroll
+    for (int u = 0; u < RING; ++u) {
+      if (k0 + u >= kp) break;
+      cb[(k0 + u) * kBuckets + tid] = c[u];
+      float m = c[u] == c[u] ? __builtin_fabsf(c[u]) : __builtin_inff();
+      m = reduce<64>(m, [](float p, float q) { return __builtin_fmaxf(p, q); });
+      if ((tid & 63) == 0) lds.largest[tid >> 6][k0 + u] = m;
+    }
+  }
+  if (tid < kp) lds.weight[tid] = merge_weight(a, trow, tid);
+  __syncthreads();
+  if (tid < 64) {
+    double m = 0.0;
+    if (tid < kp && lds.weight[tid] != 0.0) {
+      float l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) l = __builtin_fmaxf(l, lds.largest[w][tid]);
+      m = __builtin_fabs(lds.weight[tid]) * (double)l;
+    }
+    m = reduce<64>(m, [](double p, double q) { return p + q; });
+    // below 2^-960 every square is 0 in fp64
+    if (tid == 0) {
+      lds.unit = m > 0x1p-960 ? m / 2147483584.0 : m * 0.0;
+      lds.inverse = m > 0x1p-960 ? 2147483584.0 / m : 0.0;
+    }
+  }
+  __syncthreads();
+  const double unit = lds.unit, inverse = lds.inverse;
+  const bool sound = __builtin_isfinite(unit);
+#pragma unroll 4
+  for (int k = 0; k < kp; ++k) {
+    const double w = lds.weight[k];
+    const double q = w != 0.0 && sound ? __builtin_rint(w * (double)cb[k * kBuckets + tid] * inverse) : 0.0;
+    tab[k * kBuckets + tid] = (int)q;  // the thread's own words
+  }
+  __syncthreads();
+
+  double sum = 0.0;
+  for (int64_t tile = 0; tile < n_tiles; ++tile) {
+    int acc[16] = {};
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+#pragma unroll
+      for (int u = 0; u < RING; ++u) {
+        const int k = r * RING + u;
+        if (ROUNDS == 1 || k < kp) {
+          const int* tk = tab + k * kBuckets;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[4 * j + c] += tk[(ring[u][j] >> (8 * c)) & 0xffu];
+          }
+        }
+        if (r + 1 < ROUNDS) request(ring[u], tile, k + RING);
+        else request(ring[u], tile + 1, u);
+      }
+    }
+    const int64_t left = sp.end - sp.begin - tile * kTile - 16 * tid;  // of this thread's codes, the tensor's
+    if (tile + 1 == n_tiles) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] = e < left ? acc[e] : 0;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const double d = (double)acc[e];
+      sum = __fma_rn(d, d, sum);
+    }
+  }
+  sum = wave_sum(sum);
+  if ((tid & 63) == 0) lds.red[tid >> 6] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    double total = 0.0;
+    for (int w = 0; w < kWaves; ++w) total += lds.red[w];
+    a.dir_part[g.slot_base + blockIdx.x] = sound ? total * unit * unit : __builtin_nan("");
+  }
+}
+
+__device__ __forceinline__ void write_outer_norm(const OuterNormArgs& a, double sum) {
+  const double n = __builtin_sqrt(sum);
+  *a.norm = n;
+  *a.grad_scale = !__builtin_isfinite(n) ? 0.0 : n > a.max_norm ? a.max_norm / n : 1.0;
+}
+
 // k_outer_norm: the blocks' sums of squares in a fixed order -> norm and clipping factor.
 constexpr int kOuterNormThreads = 1024;
 
 __global__ __launch_bounds__(kOuterNormThreads) void k_outer_norm(const OuterNormArgs a) {
   __shared__ double red[kOuterNormThreads / 64];
   double v = 0.0;
+#pragma unroll 8
   for (int64_t b = threadIdx.x; b < a.n_slots; b += kOuterNormThreads) v += a.part[b];
   v = wave_sum(v);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -1067,9 +1194,57 @@ __global__ __launch_bounds__(kOuterNormThreads) void k_outer_norm(const OuterNor
   if (threadIdx.x == 0) {
     double sum = 0.0;
     for (int i = 0; i < kOuterNormThreads / 64; ++i) sum += red[i];
-    const double n = __builtin_sqrt(sum);
-    *a.norm = n;
-    *a.grad_scale = !__builtin_isfinite(n) ? 0.0 : n > a.max_norm ? a.max_norm / n : 1.0;
+    write_outer_norm(a, sum);
+  }
+}
+
+// k_outer_norm_one: both for a few tiles, in one block: each group of kBlock threads takes a tile at
+// a time, with fp64 tables of its own.  g: one tile a block.
+constexpr int kOneGroups = kOuterNormThreads / kBlock;
+
+__global__ __launch_bounds__(kOuterNormThreads) void k_outer_norm_one(const MergeArgs a, const LaunchGeom g,
+                                                                      const OuterNormArgs out) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ double red[kOuterNormThreads / 64];
+  const int kp = a.n_present, tid = threadIdx.x % kBlock;
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kBlock);
+  double* tab = reinterpret_cast<double*>(smem) + (size_t)group * kp * kBuckets;
+  double sum = 0.0;
+  for (int b0 = 0; b0 < g.n_blocks; b0 += kOneGroups) {
+    const int b = b0 + group;
+    int t = 0;
+    while (t + 1 < g.n_tensors && g.t[t + 1].block_first <= b) ++t;
+    const TensorDesc td = g.t[t];
+    const int64_t from = (int64_t)(b - td.block_first) * kTile;
+    const int64_t n = b < g.n_blocks ? td.numel() - from : 0;  // elements of the tile
+    const size_t trow = (size_t)g.t_base + t;
+    __syncthreads();  // the last tile's lookups are done
+    if (n > 0) {
+      for (int k = 0; k < kp; ++k) {
+        const double w = merge_weight(a, trow, k);
+        const float cb = a.codebook[((size_t)a.learner[k] * g.n_tensors_call + trow) * kBuckets + tid];
+        tab[k * kBuckets + tid] = w != 0.0 ? w * (double)cb : 0.0;
+      }
+    }
+    __syncthreads();
+    if (16 * tid < n) {  // whole: the tensor's last group of 64 codes lies within the row
+      double acc[16] = {};
+      for (int k = 0; k < kp; ++k) {
+        const vu4 q = *(const vu4*)(a.codes + (int64_t)a.learner[k] * a.stride + td.loffset() + from + 16 * tid);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] += tab[k * kBuckets + ((q[e / 4] >> (8 * (e % 4))) & 0xffu)];
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum = __fma_rn(e < n - 16 * tid ? acc[e] : 0.0, acc[e], sum);
+    }
+  }
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double total = 0.0;
+    for (int i = 0; i < kOuterNormThreads / 64; ++i) total += red[i];
+    write_outer_norm(out, total);
   }
 }
 
@@ -1192,7 +1367,7 @@ __global__ __launch_bounds__(kBlock) void k_dequant_add(const RingArgs a, const 
     const int64_t o = (valid ? tile : 0) * kTile;
     load_tile_rsrc(tile_rsrc(tl + o, valid), tid, lv[slot]);
     load_tile_rsrc(tile_rsrc(tg + o, valid), tid, gv[slot]);
-    load_codes_rsrc(src + o, valid, tid, cw[slot]);
+    load_codes_rsrc(src + o, valid ? kTile : 0, tid, cw[slot]);
   };
   auto finish = [&](int slot, int64_t tile) {
 #pragma unroll
@@ -1389,12 +1564,49 @@ hipError_t launch_rda_direction(const MergeArgs& a, const LaunchGeom& g, hipStre
   }
 }
 
+template <int RING, int ROUNDS>
+hipError_t launch_squares_r(const MergeArgs& a, const LaunchGeom& g, hipStream_t s) {
+  const size_t lds = (size_t)a.n_present * kBuckets * sizeof(int) + sizeof(SquaresLds);
+  hipError_t e = allow_lds(k_outer_squares<RING, ROUNDS>, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_outer_squares<RING, ROUNDS>), dim3(g.n_blocks), dim3(kBlock), lds, s, a, g);
+  return hipGetLastError();
+}
+
 hipError_t launch_outer_squares(const MergeArgs& a, const LaunchGeom& g, hipStream_t s) {
-  return launch_rda_direction(a, g, s);
+  static_assert(kSquaresRing == 8 && kSquaresRounds == 8, "one instantiation per ring and per number of rounds");
+  switch (a.n_present) {
+    case 1: return launch_squares_r<1, 1>(a, g, s);
+    case 2: return launch_squares_r<2, 1>(a, g, s);
+    case 3: return launch_squares_r<3, 1>(a, g, s);
+    case 4: return launch_squares_r<4, 1>(a, g, s);
+    case 5: return launch_squares_r<5, 1>(a, g, s);
+    case 6: return launch_squares_r<6, 1>(a, g, s);
+    case 7: return launch_squares_r<7, 1>(a, g, s);
+    case 8: return launch_squares_r<8, 1>(a, g, s);
+    default: break;
+  }
+  switch ((a.n_present + kSquaresRing - 1) / kSquaresRing) {
+    case 2: return launch_squares_r<8, 2>(a, g, s);
+    case 3: return launch_squares_r<8, 3>(a, g, s);
+    case 4: return launch_squares_r<8, 4>(a, g, s);
+    case 5: return launch_squares_r<8, 5>(a, g, s);
+    case 6: return launch_squares_r<8, 6>(a, g, s);
+    case 7: return launch_squares_r<8, 7>(a, g, s);
+    default: return launch_squares_r<8, 8>(a, g, s);
+  }
 }
 
 hipError_t launch_outer_norm(const OuterNormArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(k_outer_norm, dim3(1), dim3(kOuterNormThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_outer_norm_one(const MergeArgs& a, const LaunchGeom& g, const OuterNormArgs& out, hipStream_t s) {
+  const size_t lds = (size_t)kOneGroups * a.n_present * kBuckets * sizeof(double);
+  hipError_t e = allow_lds(k_outer_norm_one, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_outer_norm_one, dim3(1), dim3(kOuterNormThreads), lds, s, a, g, out);
   return hipGetLastError();
 }
 

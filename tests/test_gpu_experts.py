@@ -8,7 +8,10 @@ row's largest distance from its maximum that a probability above 2^-126 has, R(D
   * the gradient p (c - sum p c): with A the largest |c|, p A (3 R + 64 u), then the type's rounding, eps / 2 of the
     value or half its smallest subnormal;
   * counts, totals, merge weights and the step: the same operations in the same order: equal;
-  * the norm: fp64 sums in some order: relative 2^-40.
+  * the norm: fp64 sums in some order, relative 2^-40; and over more than eight tiles of 4096 elements, where a
+    learner's entries are integers of unit M / (2^31 - 64), M = sum_i |w_i| max_c |cb_i[c]| over the tensor's
+    learners: half a unit for each of K, so K M 2^-31 / 2 for an element, and by the triangle inequality the root of
+    the sum of these squares for the norm.  The factor is max_norm over it: the same, relatively.
 """
 import numpy as np
 import pytest
@@ -343,7 +346,15 @@ class Outer:
                                 max_norm=max_norm, tensor_weights=None if share is None else self.share)
         norm, scale = experts.outer_grad_norm(self.codes.cpu().numpy(), self.codebook.cpu().numpy(), self.weights,
                                               self.tensors, share, max_norm)
-        assert abs(float(self.norm) - norm) <= 2.0 ** -40 * norm and abs(float(self.scale) - scale) <= 2.0 ** -40 * scale
+        k = sum(w > 0 for w in self.weights)
+        off = 0.0
+        for t, (_, _, n) in enumerate(self.tensors):
+            w = np.array(self.weights) / sum(self.weights) if share is None else share[t]
+            m = sum(abs(w[i]) * float(self.codebook[i, t].abs().max()) for i in range(self.k) if w[i] != 0)
+            off += n * (k * m * 2.0 ** -32 * (1 + 2.0 ** -20)) ** 2
+        tiles = sum(-(-n // 4096) for _, _, n in self.tensors)
+        tol = 2.0 ** -40 * norm + (off ** 0.5 if tiles > 8 or k > 16 else 0.0)
+        assert abs(float(self.norm) - norm) <= tol and abs(float(self.scale) - scale) <= 2 * tol / norm * scale + 2.0 ** -52
         return float(self.scale)
 
     def check_step(self, share, scale):
@@ -392,8 +403,9 @@ def test_without_weights_and_factor_it_is_the_outer_step():
     assert torch.equal(th, o.theta) and torch.equal(mo, o.mom)
 
 
-def test_a_gradient_that_is_not_finite_is_left_out():
-    o = Outer(LISTS["edges"], 2)
+@pytest.mark.parametrize("sizes", [LISTS["edges"], LISTS["ragged"]])
+def test_a_gradient_that_is_not_finite_is_left_out(sizes):
+    o = Outer(sizes, 2)
     o.codebook[1, 3, :] = float("inf")
     dlc.dlc_outer_grad_norm(o.codes, o.codebook, o.weights, o.tensors, o.norm, o.scale, o.ws, max_norm=1.0)
     assert not torch.isfinite(o.norm) and float(o.scale) == 0.0
@@ -405,8 +417,30 @@ def test_a_gradient_that_is_not_finite_is_left_out():
 def test_a_gradient_of_zero_has_norm_zero_and_is_not_clipped():
     o = Outer([100, 5000], 2)
     o.codebook.zero_()
-    o.check_norm(None, 1.0)
+    dlc.dlc_outer_grad_norm(o.codes, o.codebook, o.weights, o.tensors, o.norm, o.scale, o.ws, max_norm=1.0)
     assert float(o.norm) == 0.0 and float(o.scale) == 1.0
+    o = Outer([100, 5000, 70000], 2)
+    o.codebook.zero_()
+    dlc.dlc_outer_grad_norm(o.codes, o.codebook, o.weights, o.tensors, o.norm, o.scale, o.ws, max_norm=1.0)
+    assert float(o.norm) == 0.0 and float(o.scale) == 1.0
+
+
+@pytest.mark.parametrize("sizes", [[2000], [100000, 3, 4097]])
+@pytest.mark.parametrize("size", [1e-44, 1e-20, 1e20, 3e38])
+def test_codebooks_of_every_size(sizes, size):
+    """From subnormal entries to the largest, one tensor's far from another's."""
+    o = Outer(sizes, 3, seed=4)
+    o.codebook.mul_(size / float(o.codebook.abs().max()))
+    o.codebook[:, -1] *= 0.125
+    o.check_norm(None, size)
+
+
+def test_learners_that_nearly_cancel():
+    o = Outer([70000], 2, weights=[1.0, 1.0])
+    o.codes[1].copy_(o.codes[0])
+    o.codebook[1].copy_(-o.codebook[0])
+    o.codebook[1, 0, 7] *= 1 + 2.0 ** -20
+    o.check_norm(None)
 
 
 def test_experts_that_nobody_used_and_learners_that_did_not():
