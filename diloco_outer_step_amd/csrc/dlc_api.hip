@@ -125,7 +125,13 @@ constexpr int64_t kMergeTilesPerBlock = 2;
 // each block first builds its K scaled codebook tables: it does best with
 // coarser blocks than the merge.
 constexpr int64_t kDirectionBlocks = 16384;
+// Squares of the merged gradient: 1B set, K = 8: 16384 blocks 1059 us, 8192 1069, 4096 1112, 32768 1075;
+// fragment of 4.6M parameters, K = 4 and 14: at least 2 tiles a block 12.1 and 25.3 us, 1 tile 12.9 and 26.4, 4
+// tiles 12.8 and 29.1.
 constexpr int64_t kSquaresBlocks = 16384;
+constexpr int64_t kSquaresMinTiles = 2;
+// With so many blocks the entries' errors average out in k_outer_squares; fewer have fp64 tables.
+constexpr int64_t kExactSquares = 256;
 constexpr int64_t kBroadcastBlocks = 8192;
 // The merged gradient's norm over so few tiles runs in one block (four tiles at a time, one launch
 // instead of two) as long as its tables fit in LDS.
@@ -214,7 +220,7 @@ Partition direction_partition(const dlc_tensor* t, int32_t n) {
 
 // The merged gradient's squares: as the direction pass, blocks that first build their tables.
 Partition squares_partition(const dlc_tensor* t, int32_t n) {
-  return make_partition(t, n, kUnlimitedTiles, kSquaresBlocks);
+  return make_partition(t, n, kUnlimitedTiles, kSquaresBlocks, 1, kSquaresMinTiles);
 }
 
 // merge blocks work on kMergeTiles tiles side by side, kMergeTilesPerBlock in all
@@ -1300,13 +1306,15 @@ int32_t dlc_outer_grad_norm(const uint8_t* codes, int64_t learner_stride, int32_
     a.dir_part = static_cast<double*>(workspace);
     const hipStream_t st = static_cast<hipStream_t>(hip_stream);
     const dlc::OuterNormArgs out{a.dir_part, norm, grad_scale, max_norm, p.n_slots};
-    // few tiles are one to a block in this partition
-    if (p.n_slots <= kOneNormTiles && a.n_present <= kOneNormLearners && p.launches[0].tiles_per_block == 1) {
-      const hipError_t e = dlc::launch_outer_norm_one(a, p.launches[0], out, st);
-      return e != hipSuccess ? hip_fail(e, "outer gradient norm kernel launch") : ok();
+    if (p.n_slots <= kOneNormTiles && a.n_present <= kOneNormLearners) {
+      const Partition tiles = make_partition(tensors, n_tensors, 1, kUnlimitedTiles);
+      if (tiles.n_slots <= kOneNormTiles) {  // so one launch
+        const hipError_t e = dlc::launch_outer_norm_one(a, tiles.launches[0], out, st);
+        return e != hipSuccess ? hip_fail(e, "outer gradient norm kernel launch") : ok();
+      }
     }
     for (const dlc::LaunchGeom& g : p.launches) {
-      const hipError_t e = dlc::launch_outer_squares(a, g, st);
+      const hipError_t e = p.n_slots < kExactSquares ? dlc::launch_rda_direction(a, g, st) : dlc::launch_outer_squares(a, g, st);
       if (e != hipSuccess) return hip_fail(e, "outer gradient kernel launch");
     }
     const hipError_t e = dlc::launch_outer_norm(out, st);

@@ -872,7 +872,8 @@ __device__ __forceinline__ double rda_unit_weight(const MergeArgs& a, const Laun
 }
 
 //
-// The clipped step's table holds scale * w * codebook_i[c] with the tensor's own weights w.
+// The clipped step's table holds scale * w * codebook_i[c] with the tensor's own weights
+// w, and DIR without norm2 sums the squares of the merged gradient with them.
 __device__ __forceinline__ double merge_weight(const MergeArgs& a, size_t trow, int k) {
   return a.tensor_w != nullptr ? a.tensor_w[trow * a.n_learners + a.learner[k]] : a.w_hat[k];
 }
@@ -896,7 +897,7 @@ __global__ __launch_bounds__(kMergeBlock) __attribute__((amdgpu_waves_per_eu(4))
     const int k = i >> 8, c = i & (kBuckets - 1);
     const float cb = a.codebook[((size_t)a.learner[k] * g.n_tensors_call + trow) * kBuckets + c];
     double w;
-    if (DIR) w = rda_unit_weight(a, g, trow, k);
+    if (DIR) w = a.norm2 != nullptr ? rda_unit_weight(a, g, trow, k) : merge_weight(a, trow, k);
     else w = a.coef != nullptr ? a.coef[trow * kp + k] : scale * merge_weight(a, trow, k);
     tab[i] = w != 0.0 ? w * (double)cb : 0.0;  // a weight of 0 leaves the learner out, whatever its codebook holds
   }
@@ -1043,11 +1044,13 @@ __global__ __launch_bounds__(kBuckets) void k_rda_coef(const MergeArgs a, const 
 //
 // What bounds it is LDS: one lookup for each code.  fp64 tables take 4.75 clocks a wave's lookup (two passes
 // of 32 lanes, and conflicts: 98% of the kernel's time), 32-bit ones about 3.5.  So an entry is a
-// 32-bit integer, round(w_i cb_i[c] / unit), unit = M / (2^31 - 64), M = sum_i |w_i| max_c |cb_i[c]|:
+// 32-bit integer, w_i cb_i[c] / unit rounded, unit = M / (2^31 - 64), M = sum_i |w_i| max_c |cb_i[c]|:
 // no sum over the learners can overflow, integers add in one instruction and without error, and
-// g is off by at most K / 2 units, K 2^-32 of M: 2^-26 of it at the most that a call takes, where an
-// fp32 entry would be off by 2^-24 of itself.  Squares are summed in fp64.  An entry that is not
-// finite, whether a code refers to it or not, makes the sum NaN.
+// g is off by less than K units, K 2^-31 of M.  Squares are summed in fp64.  An entry serves a
+// hundredth of a tensor's elements, whose errors would add up: each block rounds its entries up or
+// down by pseudo-random bits of its own, so that they average out over the blocks (the norm of the 1B
+// set at K = 8 is off by 2^-40 of itself).  Fewer blocks take fp64 tables (k_merge, DIR).  An entry that
+// is not finite, whether a code refers to it or not, makes the sum NaN.
 //
 // A thread holds 16 consecutive codes of every learner (16-byte loads).  Up to 8 learners: a learner's
 // codes of the next tile are requested as soon as its codes of this one are looked up, so
@@ -1062,6 +1065,13 @@ struct SquaresLds {
   double unit, inverse;
   double red[kWaves];
 };
+
+// Multiplies and folds: every bit of the result depends on every bit of x.
+__device__ __forceinline__ uint32_t mixed(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x9E3779B9u;
+  x = (x ^ (x >> 15)) * 0x6A09E667u;
+  return x ^ (x >> 16);
+}
 
 // RING learners a round, ROUNDS rounds a tile.
 template <int RING, int ROUNDS>
@@ -1128,7 +1138,8 @@ __global__ __launch_bounds__(kBlock) void k_outer_squares(const MergeArgs a, con
 #pragma unroll 4
   for (int k = 0; k < kp; ++k) {
     const double w = lds.weight[k];
-    const double q = w != 0.0 && sound ? __builtin_rint(w * (double)cb[k * kBuckets + tid] * inverse) : 0.0;
+    const uint32_t bits = mixed(mixed((uint32_t)(g.slot_base + blockIdx.x)) + (uint32_t)(k * kBuckets + tid));
+    const double q = w != 0.0 && sound ? __builtin_floor(w * (double)cb[k * kBuckets + tid] * inverse + bits * 0x1p-32) : 0.0;
     tab[k * kBuckets + tid] = (int)q;  // the thread's own words
   }
   __syncthreads();
@@ -1517,9 +1528,17 @@ hipError_t launch_codebook(const QuantArgs& a, const LaunchGeom& g, hipStream_t 
   return hipGetLastError();
 }
 
+// With few learners three blocks a CU have more than enough loads under way, and memory serves what
+// three of them work on faster than what four do: the LDS that they ask for and do not use sees
+// to that.  Clipped step of the 1B set, four blocks against three, us: K = 3 2901, 2870; 4 3092, 2920; 5 3189, 3118;
+// 1 and 2 the same; 6 3216, 3276; 8 3432, 3567.  (Two: 4 2912, 5 3058, but 23.1 against 22.1 on a 4.6M fragment.)
+constexpr size_t kFewLearnersLds = 53000;
+constexpr int kFewLearners = 5;
+
 template <int NR>
 hipError_t launch_merge_r(const MergeArgs& a, const LaunchGeom& g, hipStream_t s) {
-  const size_t lds = (size_t)a.n_present * kBuckets * sizeof(double);
+  const size_t tables = (size_t)a.n_present * kBuckets * sizeof(double);
+  const size_t lds = a.n_present <= kFewLearners ? kFewLearnersLds : tables;
   hipError_t e = allow_lds(k_merge<NR>, lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_merge<NR>, dim3(g.n_blocks), dim3(kMergeBlock), lds, s, a, g);

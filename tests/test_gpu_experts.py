@@ -8,10 +8,10 @@ row's largest distance from its maximum that a probability above 2^-126 has, R(D
   * the gradient p (c - sum p c): with A the largest |c|, p A (3 R + 64 u), then the type's rounding, eps / 2 of the
     value or half its smallest subnormal;
   * counts, totals, merge weights and the step: the same operations in the same order: equal;
-  * the norm: fp64 sums in some order, relative 2^-40; and over more than eight tiles of 4096 elements, where a
+  * the norm: fp64 sums in some order, relative 2^-40; and from 256 blocks of two tiles of 4096 elements on, where a
     learner's entries are integers of unit M / (2^31 - 64), M = sum_i |w_i| max_c |cb_i[c]| over the tensor's
-    learners: half a unit for each of K, so K M 2^-31 / 2 for an element, and by the triangle inequality the root of
-    the sum of these squares for the norm.  The factor is max_norm over it: the same, relatively.
+    learners: a unit at most for each of K, so K M 2^-31 for an element, and by the triangle inequality the root of the
+    sum of these squares for the norm.  The factor is max_norm over it: the same, relatively.
 """
 import numpy as np
 import pytest
@@ -351,9 +351,9 @@ class Outer:
         for t, (_, _, n) in enumerate(self.tensors):
             w = np.array(self.weights) / sum(self.weights) if share is None else share[t]
             m = sum(abs(w[i]) * float(self.codebook[i, t].abs().max()) for i in range(self.k) if w[i] != 0)
-            off += n * (k * m * 2.0 ** -32 * (1 + 2.0 ** -20)) ** 2
-        tiles = sum(-(-n // 4096) for _, _, n in self.tensors)
-        tol = 2.0 ** -40 * norm + (off ** 0.5 if tiles > 8 or k > 16 else 0.0)
+            off += n * (k * m * 2.0 ** -31 * (1 + 2.0 ** -20)) ** 2
+        blocks = sum(-(-n // 8192) for _, _, n in self.tensors)
+        tol = 2.0 ** -40 * norm + (off ** 0.5 if blocks >= 256 else 0.0)
         assert abs(float(self.norm) - norm) <= tol and abs(float(self.scale) - scale) <= 2 * tol / norm * scale + 2.0 ** -52
         return float(self.scale)
 
@@ -367,7 +367,7 @@ class Outer:
         assert np.array_equal(self.theta.cpu().numpy(), th) and np.array_equal(self.mom.cpu().numpy(), mo)
 
 
-LISTS = {"one": [1], "vectors": [4096] * 4, "edges": [63, 64, 65, 4095, 4096, 4097, 8191, 8193, 1, 2],
+LISTS = {"integer_tables": [1 << 21, 3, 500_001, 70_000], "one": [1], "vectors": [4096] * 4, "edges": [63, 64, 65, 4095, 4096, 4097, 8191, 8193, 1, 2],
          "ragged": [1, 100003, 65, 64 * 300 + 9, 31, 77777], "many": [(37 * i) % 700 + 1 for i in range(400)]}
 
 
@@ -403,7 +403,7 @@ def test_without_weights_and_factor_it_is_the_outer_step():
     assert torch.equal(th, o.theta) and torch.equal(mo, o.mom)
 
 
-@pytest.mark.parametrize("sizes", [LISTS["edges"], LISTS["ragged"]])
+@pytest.mark.parametrize("sizes", [LISTS["edges"], LISTS["ragged"], LISTS["integer_tables"]])
 def test_a_gradient_that_is_not_finite_is_left_out(sizes):
     o = Outer(sizes, 2)
     o.codebook[1, 3, :] = float("inf")
@@ -419,13 +419,13 @@ def test_a_gradient_of_zero_has_norm_zero_and_is_not_clipped():
     o.codebook.zero_()
     dlc.dlc_outer_grad_norm(o.codes, o.codebook, o.weights, o.tensors, o.norm, o.scale, o.ws, max_norm=1.0)
     assert float(o.norm) == 0.0 and float(o.scale) == 1.0
-    o = Outer([100, 5000, 70000], 2)
+    o = Outer([100, 5000, 2_170_000], 2)
     o.codebook.zero_()
     dlc.dlc_outer_grad_norm(o.codes, o.codebook, o.weights, o.tensors, o.norm, o.scale, o.ws, max_norm=1.0)
     assert float(o.norm) == 0.0 and float(o.scale) == 1.0
 
 
-@pytest.mark.parametrize("sizes", [[2000], [100000, 3, 4097]])
+@pytest.mark.parametrize("sizes", [[2000], [100000, 3, 4097], [2_200_000, 3, 4097]])
 @pytest.mark.parametrize("size", [1e-44, 1e-20, 1e20, 3e38])
 def test_codebooks_of_every_size(sizes, size):
     """From subnormal entries to the largest, one tensor's far from another's."""
@@ -435,8 +435,9 @@ def test_codebooks_of_every_size(sizes, size):
     o.check_norm(None, size)
 
 
-def test_learners_that_nearly_cancel():
-    o = Outer([70000], 2, weights=[1.0, 1.0])
+@pytest.mark.parametrize("n", [70000, 2_300_000])
+def test_learners_that_nearly_cancel(n):
+    o = Outer([n], 2, weights=[1.0, 1.0])
     o.codes[1].copy_(o.codes[0])
     o.codebook[1].copy_(-o.codebook[0])
     o.codebook[1, 0, 7] *= 1 + 2.0 ** -20
