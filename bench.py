@@ -73,7 +73,7 @@ def parse():
                          "and print them as one JSON line")
     ap.add_argument("--reported-only", default=None,
                     help="comma-separated subset of c1,c4_largest,c2,c5k1,c5k16,native_c2,native_c5k1,"
-                         "broadcast_c3,stale_c3,ring_study,ring_c3,rda_c3,inner_c3")
+                         "broadcast_c3,stale_c3,ring_study,ring_c3,rda_c3,inner_c3,clipped_c3")
     ap.add_argument("--copy-probe", action="store_true",
                     help="only run a device-to-device copy of known size (counter calibration)")
     return ap.parse_args()
@@ -643,15 +643,56 @@ def inner_rate(key, device, reps=10, warmup=3):
     return out
 
 
+def clipped_rate(key, device, reps=10, warmup=3):
+    """The clipped outer step of a set: the merged gradient's norm (K bytes per parameter) and the step with its factor
+    (16 + K), after one quantization."""
+    import statistics
+    import torch
+    import diloco_outer_step_amd as dlc
+    import workloads
+    cfg = workloads.config(key)
+    inp = workloads.fragment_inputs(cfg, list(range(len(cfg.tensors))), device)
+    k, stride = inp.theta_L.shape
+    plan = dlc.TensorList(inp.tensors)
+    codes, codebook, rng = dlc.outputs_for(k, stride, len(plan), device)
+    dlc.dlc_quantize(inp.theta_g, inp.theta_L, plan, codes, codebook, rng, dlc.alloc_workspace(k, plan, device))
+    norm, scale = (torch.zeros(1, dtype=torch.float64, device=device) for _ in range(2))
+    ws = dlc.alloc_outer_grad_norm_workspace(plan, device)
+    theta, momentum = inp.theta_g.clone(), torch.zeros_like(inp.theta_g)
+    calls = {
+        "norm": (k, lambda: dlc.dlc_outer_grad_norm(codes, codebook, inp.weights, plan, norm, scale, ws, max_norm=1.0)),
+        "step": (16 + k, lambda: dlc.dlc_merge_clipped_step(theta, momentum, codes, codebook, inp.weights, plan,
+                                                            grad_scale=scale)),
+    }
+    n = sum(x for _, _, x in inp.tensors)
+    out = dict(workload=cfg.title, n_params=n, k_present=k)
+    for name, (per, run) in calls.items():
+        for _ in range(warmup):
+            run()
+        torch.cuda.synchronize()
+        ts = []
+        for _ in range(reps):
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            e0.record()
+            run()
+            e1.record()
+            torch.cuda.synchronize()
+            ts.append(e0.elapsed_time(e1))
+        ms_ = statistics.median(ts)
+        out[name] = dict(ms=ms_, bytes_per_param=per, hbm_gbps=per * n / (ms_ * 1e-3) / 1e9,
+                         hbm_frac=per * n / (ms_ * 1e-3) / 1e9 / PEAK_HBM_GBPS)
+    return out
+
+
 def reported(device, only=None):
     """The parameter sets that are reported but not gated: the 4096^2 tensor (cold
     cache), the 10B set's largest fragment, full 24-fragment cycles of the 135M set
     and of the edge mix, the calls of the next rows on the 1B set, and the learners'
-    inner step on it."""
+    inner step and the clipped outer step on it."""
     import torch
     keys = only.split(",") if only else ["c1", "c4_largest", "c2", "c5k1", "c5k16", "native_c2", "native_c5k1",
                                          "broadcast_c3",
-                                         "stale_c3", "ring_study", "ring_c3", "rda_c3", "inner_c3"]
+                                         "stale_c3", "ring_study", "ring_c3", "rda_c3", "inner_c3", "clipped_c3"]
     out = {}
     if "c1" in keys:
         out["c1"] = single_call_cold("c1", device)
@@ -681,6 +722,11 @@ def reported(device, only=None):
         torch.cuda.empty_cache()
         print("# inner step c3: " + ", ".join(f"{n} {v['ms']:.3f} ms" for n, v in out["inner_c3"].items()
                                               if isinstance(v, dict)), file=sys.stderr, flush=True)
+    if "clipped_c3" in keys:
+        out["clipped_c3"] = clipped_rate("c3", device)
+        torch.cuda.empty_cache()
+        print("# clipped step c3: " + ", ".join(f"{n} {v['ms']:.3f} ms" for n, v in out["clipped_c3"].items()
+                                                if isinstance(v, dict)), file=sys.stderr, flush=True)
     if "ring_study" in keys:
         out["ring_study"] = ring_study(device)
         torch.cuda.empty_cache()

@@ -125,16 +125,15 @@ constexpr int64_t kMergeTilesPerBlock = 2;
 // each block first builds its K scaled codebook tables: it does best with
 // coarser blocks than the merge.
 constexpr int64_t kDirectionBlocks = 16384;
-// Squares of the merged gradient: 1B set, K = 8: 16384 blocks 1059 us, 8192 1069, 4096 1112, 32768 1075;
-// fragment of 4.6M parameters, K = 4 and 14: at least 2 tiles a block 12.1 and 25.3 us, 1 tile 12.9 and 26.4, 4
-// tiles 12.8 and 29.1.
+// Squares of the merged gradient: 1B set, K = 8: 16384 blocks 1172 us, 8192 1179, 4096 1197, 32768 1191;
+// fragment of 4.6M parameters, K = 4 and 14: at least 2 tiles a block 11.1 and 24.3 us, 1 tile 12.1 and 23.1 (4
+// tiles were slower than either, 12.8 and 29.1, in an earlier form).
 constexpr int64_t kSquaresBlocks = 16384;
 constexpr int64_t kSquaresMinTiles = 2;
-// With so many blocks the entries' errors average out in k_outer_squares; fewer have fp64 tables.
-constexpr int64_t kExactSquares = 256;
 constexpr int64_t kBroadcastBlocks = 8192;
-// The merged gradient's norm over so few tiles runs in one block (four tiles at a time, one launch
-// instead of two) as long as its tables fit in LDS.
+// The merged gradient's norm over so few tiles runs in one block (four tiles at a time, one launch instead of
+// two: four vectors of 4096, K = 2, 8.0 against 10.8 us a call, replayed from a graph 5.8 against 6.9) as
+// long as its tables fit in LDS.
 constexpr int64_t kOneNormTiles = 8;
 constexpr int32_t kOneNormLearners = 16;
 // At least one full group of 4 tiles per statistics or encode block: on a
@@ -1314,7 +1313,7 @@ int32_t dlc_outer_grad_norm(const uint8_t* codes, int64_t learner_stride, int32_
       }
     }
     for (const dlc::LaunchGeom& g : p.launches) {
-      const hipError_t e = p.n_slots < kExactSquares ? dlc::launch_rda_direction(a, g, st) : dlc::launch_outer_squares(a, g, st);
+      const hipError_t e = dlc::launch_outer_squares(a, g, st);
       if (e != hipSuccess) return hip_fail(e, "outer gradient kernel launch");
     }
     const hipError_t e = dlc::launch_outer_norm(out, st);

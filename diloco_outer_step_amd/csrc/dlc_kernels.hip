@@ -16,6 +16,8 @@
 //   k_merge<NR, true>, k_rda_coef
 //                   Radial-Directional Averaging: the squared norm of the averaged
 //                   direction per block, then per-(tensor, learner) coefficients
+//   k_outer_squares, k_outer_norm, k_outer_norm_one
+//                   the merged gradient's norm and its clipping factor, which k_merge takes
 //   k_dequant_add   one hop of the ring that requantizes at every hop: the receiver
 //                   adds the dequantized message to its pseudo-gradient and forms the
 //                   statistics partials of its next message
@@ -40,7 +42,6 @@
 // (checked against the exact division near bucket edges) and the fixed-point
 // histogram position.
 #include "dlc_internal.h"
-#include "dlc_lanes.h"
 
 #include <cfloat>
 #include <type_traits>
@@ -872,8 +873,7 @@ __device__ __forceinline__ double rda_unit_weight(const MergeArgs& a, const Laun
 }
 
 //
-// The clipped step's table holds scale * w * codebook_i[c] with the tensor's own weights
-// w, and DIR without norm2 sums the squares of the merged gradient with them.
+// The clipped step's table holds scale * w * codebook_i[c] with the tensor's own weights w.
 __device__ __forceinline__ double merge_weight(const MergeArgs& a, size_t trow, int k) {
   return a.tensor_w != nullptr ? a.tensor_w[trow * a.n_learners + a.learner[k]] : a.w_hat[k];
 }
@@ -897,7 +897,7 @@ __global__ __launch_bounds__(kMergeBlock) __attribute__((amdgpu_waves_per_eu(4))
     const int k = i >> 8, c = i & (kBuckets - 1);
     const float cb = a.codebook[((size_t)a.learner[k] * g.n_tensors_call + trow) * kBuckets + c];
     double w;
-    if (DIR) w = a.norm2 != nullptr ? rda_unit_weight(a, g, trow, k) : merge_weight(a, trow, k);
+    if (DIR) w = rda_unit_weight(a, g, trow, k);
     else w = a.coef != nullptr ? a.coef[trow * kp + k] : scale * merge_weight(a, trow, k);
     tab[i] = w != 0.0 ? w * (double)cb : 0.0;  // a weight of 0 leaves the learner out, whatever its codebook holds
   }
@@ -1040,148 +1040,101 @@ __global__ __launch_bounds__(kBuckets) void k_rda_coef(const MergeArgs a, const 
 
 // ---------------------------------------------------------------------------
 // k_outer_squares: the sum of squares of the merged gradient per block, from the codes alone
-// (K bytes a parameter).
+// (K bytes a parameter), through the merge's fp64 tables.
 //
-// What bounds it is LDS: one lookup for each code.  fp64 tables take 4.75 clocks a wave's lookup (two passes
-// of 32 lanes, and conflicts: 98% of the kernel's time), 32-bit ones about 3.5.  So an entry is a
-// 32-bit integer, w_i cb_i[c] / unit rounded, unit = M / (2^31 - 64), M = sum_i |w_i| max_c |cb_i[c]|:
-// no sum over the learners can overflow, integers add in one instruction and without error, and
-// g is off by less than K units, K 2^-31 of M.  Squares are summed in fp64.  An entry serves a
-// hundredth of a tensor's elements, whose errors would add up: each block rounds its entries up or
-// down by pseudo-random bits of its own, so that they average out over the blocks (the norm of the 1B
-// set at K = 8 is off by 2^-40 of itself).  Fewer blocks take fp64 tables (k_merge, DIR).  An entry that
-// is not finite, whether a code refers to it or not, makes the sum NaN.
+// What bounds it is LDS: one lookup for each code, 32 lanes a clock and as often again as two of them meet
+// in a bank, 4.75 clocks a wave's lookup: 98% of the kernel's time.  1B set, K = 8 (6.8 GB): 1.165 ms a call, 5.9 TB/s.
+// 32-bit integer tables take the same clocks; their additions draw less power, the clock rises, and the call took
+// 1.07 ms, but their roundings have to be kept from adding up and smaller calls were slower (12.1 against 11.2 us
+// for a fragment of 4.6M parameters, K = 4).
 //
-// A thread holds 16 consecutive codes of every learner (16-byte loads).  Up to 8 learners: a learner's
-// codes of the next tile are requested as soon as its codes of this one are looked up, so
-// K KB a wave are always under way.  More learners take rounds of 8, padded with null requests.
+// A thread holds 16 consecutive codes of every learner (16-byte loads).  Up to 4 learners: a learner's
+// codes of the next tile are requested as soon as its codes of this one are looked up, so K KB a wave
+// are always under way.  More learners take rounds of 4, padded with null requests (rounds of 8 are
+// the same at K = 8 and 5% slower at 14, with 98 registers for 72).
 // ---------------------------------------------------------------------------
-constexpr int kSquaresRing = 8;
-constexpr int kSquaresRounds = kMaxLearners / kSquaresRing;
+constexpr int kSquaresRing = 4;
 
-struct SquaresLds {
-  float largest[kWaves][kMaxLearners];
-  double weight[kMaxLearners];
-  double unit, inverse;
-  double red[kWaves];
-};
-
-// Multiplies and folds: every bit of the result depends on every bit of x.
-__device__ __forceinline__ uint32_t mixed(uint32_t x) {
-  x = (x ^ (x >> 16)) * 0x9E3779B9u;
-  x = (x ^ (x >> 15)) * 0x6A09E667u;
-  return x ^ (x >> 16);
-}
-
-// RING learners a round, ROUNDS rounds a tile.
-template <int RING, int ROUNDS>
+// RING learners a round; MANY: as many rounds a tile as the learners need.
+template <int RING, bool MANY>
 __global__ __launch_bounds__(kBlock) void k_outer_squares(const MergeArgs a, const LaunchGeom g) {
   extern __shared__ __align__(16) unsigned char smem[];
-  int* tab = reinterpret_cast<int*>(smem);
-  SquaresLds& lds = *reinterpret_cast<SquaresLds*>(smem + (size_t)a.n_present * kBuckets * sizeof(int));
+  __shared__ double red[kWaves];
+  double* tab = reinterpret_cast<double*>(smem);
   const int kp = a.n_present, tid = threadIdx.x;
   const Span sp = block_span(g);
   const TensorDesc td = g.t[sp.t];
   const size_t trow = (size_t)g.row_base + g.t_base + sp.t;
   const int64_t n_tiles = (sp.end - sp.begin + kTile - 1) / kTile;
+  // lane k holds where learner k's codes of this block begin: a scalar load in the loop would wait for
+  // the lookups as well
+  const int lane = tid & 63;
+  const uint64_t row = (uint64_t)(a.codes + (int64_t)a.learner[lane < kp ? lane : kp - 1] * a.stride + td.loffset() + sp.begin);
   // codes of (tile, learner), 16 for each thread: what lies behind the tensor in its last group of 64 is read too
   const auto request = [&](vu4& dst, int64_t tile, int k) {
     const bool valid = k < kp && tile < n_tiles;
-    const int64_t from = sp.begin + (valid ? tile : 0) * kTile;
-    const uint8_t* p = a.codes + (int64_t)a.learner[k < kp ? k : kp - 1] * a.stride + td.loffset() + from;
-    const int64_t left = (sp.end - from + 63) & ~(int64_t)63;
+    const int64_t from = valid ? tile * kTile : 0;
+    const uint64_t p = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(row >> 32), k) << 32 |
+                       (uint32_t)__builtin_amdgcn_readlane((int)row, k);
+    const int64_t left = (sp.end - sp.begin - from + 63) & ~(int64_t)63;
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(p), (short)0, valid ? (int)(left < kTile ? left : kTile) : 0, kBufferWord3);
+        reinterpret_cast<uint8_t*>(p + from), (short)0, valid ? (int)(left < kTile ? left : kTile) : 0, kBufferWord3);
     dst = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, tid * 16, 0, 2));
   };
   vu4 ring[RING];
 #pragma unroll
   for (int u = 0; u < RING; ++u) request(ring[u], 0, u);
 
-  float* cb = reinterpret_cast<float*>(tab);
   for (int k0 = 0; k0 < kp; k0 += RING) {
-    float c[RING];
+    float cb[RING];
 #pragma unroll
     for (int u = 0; u < RING; ++u) {
       const int k = k0 + u < kp ? k0 + u : kp - 1;
-      c[u] = a.codebook[((size_t)a.learner[k] * g.n_tensors_call + trow) * kBuckets + tid];
+      cb[u] = a.codebook[((size_t)a.learner[k] * g.n_tensors_call + trow) * kBuckets + tid];
     }
 #pragma unroll
     for (int u = 0; u < RING; ++u) {
       if (k0 + u >= kp) break;
-      cb[(k0 + u) * kBuckets + tid] = c[u];
-      float m = c[u] == c[u] ? __builtin_fabsf(c[u]) : __builtin_inff();
-      m = reduce<64>(m, [](float p, float q) { return __builtin_fmaxf(p, q); });
-      if ((tid & 63) == 0) lds.largest[tid >> 6][k0 + u] = m;
+      const double w = merge_weight(a, trow, k0 + u);
+      tab[(k0 + u) * kBuckets + tid] = w != 0.0 ? w * (double)cb[u] : 0.0;
     }
-  }
-  if (tid < kp) lds.weight[tid] = merge_weight(a, trow, tid);
-  __syncthreads();
-  if (tid < 64) {
-    double m = 0.0;
-    if (tid < kp && lds.weight[tid] != 0.0) {
-      float l = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) l = __builtin_fmaxf(l, lds.largest[w][tid]);
-      m = __builtin_fabs(lds.weight[tid]) * (double)l;
-    }
-    m = reduce<64>(m, [](double p, double q) { return p + q; });
-    // below 2^-960 every square is 0 in fp64
-    if (tid == 0) {
-      lds.unit = m > 0x1p-960 ? m / 2147483584.0 : m * 0.0;
-      lds.inverse = m > 0x1p-960 ? 2147483584.0 / m : 0.0;
-    }
-  }
-  __syncthreads();
-  const double unit = lds.unit, inverse = lds.inverse;
-  const bool sound = __builtin_isfinite(unit);
-#pragma unroll 4
-  for (int k = 0; k < kp; ++k) {
-    const double w = lds.weight[k];
-    const uint32_t bits = mixed(mixed((uint32_t)(g.slot_base + blockIdx.x)) + (uint32_t)(k * kBuckets + tid));
-    const double q = w != 0.0 && sound ? __builtin_floor(w * (double)cb[k * kBuckets + tid] * inverse + bits * 0x1p-32) : 0.0;
-    tab[k * kBuckets + tid] = (int)q;  // the thread's own words
   }
   __syncthreads();
 
   double sum = 0.0;
   for (int64_t tile = 0; tile < n_tiles; ++tile) {
-    int acc[16] = {};
-#pragma unroll
-    for (int r = 0; r < ROUNDS; ++r) {
+    double acc[16] = {};
+    for (int k0 = 0; k0 < kp; k0 += RING) {  // one round unless MANY
+      const bool more = MANY && k0 + RING < kp;
 #pragma unroll
       for (int u = 0; u < RING; ++u) {
-        const int k = r * RING + u;
-        if (ROUNDS == 1 || k < kp) {
-          const int* tk = tab + k * kBuckets;
+        if (!MANY || k0 + u < kp) {
+          const double* tk = tab + (k0 + u) * kBuckets;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[4 * j + c] += tk[(ring[u][j] >> (8 * c)) & 0xffu];
           }
         }
-        if (r + 1 < ROUNDS) request(ring[u], tile, k + RING);
-        else request(ring[u], tile + 1, u);
+        request(ring[u], more ? tile : tile + 1, more ? k0 + RING + u : u);
       }
+      if (!MANY) break;
     }
     const int64_t left = sp.end - sp.begin - tile * kTile - 16 * tid;  // of this thread's codes, the tensor's
     if (tile + 1 == n_tiles) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[e] = e < left ? acc[e] : 0;
+      for (int e = 0; e < 16; ++e) acc[e] = e < left ? acc[e] : 0.0;
     }
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const double d = (double)acc[e];
-      sum = __fma_rn(d, d, sum);
-    }
+    for (int e = 0; e < 16; ++e) sum = __fma_rn(acc[e], acc[e], sum);
   }
   sum = wave_sum(sum);
-  if ((tid & 63) == 0) lds.red[tid >> 6] = sum;
+  if ((tid & 63) == 0) red[tid >> 6] = sum;
   __syncthreads();
   if (tid == 0) {
     double total = 0.0;
-    for (int w = 0; w < kWaves; ++w) total += lds.red[w];
-    a.dir_part[g.slot_base + blockIdx.x] = sound ? total * unit * unit : __builtin_nan("");
+    for (int w = 0; w < kWaves; ++w) total += red[w];
+    a.dir_part[g.slot_base + blockIdx.x] = total;
   }
 }
 
@@ -1583,36 +1536,23 @@ hipError_t launch_rda_direction(const MergeArgs& a, const LaunchGeom& g, hipStre
   }
 }
 
-template <int RING, int ROUNDS>
+template <int RING, bool MANY>
 hipError_t launch_squares_r(const MergeArgs& a, const LaunchGeom& g, hipStream_t s) {
-  const size_t lds = (size_t)a.n_present * kBuckets * sizeof(int) + sizeof(SquaresLds);
-  hipError_t e = allow_lds(k_outer_squares<RING, ROUNDS>, lds);
+  const size_t lds = (size_t)a.n_present * kBuckets * sizeof(double);
+  hipError_t e = allow_lds(k_outer_squares<RING, MANY>, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_outer_squares<RING, ROUNDS>), dim3(g.n_blocks), dim3(kBlock), lds, s, a, g);
+  hipLaunchKernelGGL((k_outer_squares<RING, MANY>), dim3(g.n_blocks), dim3(kBlock), lds, s, a, g);
   return hipGetLastError();
 }
 
 hipError_t launch_outer_squares(const MergeArgs& a, const LaunchGeom& g, hipStream_t s) {
-  static_assert(kSquaresRing == 8 && kSquaresRounds == 8, "one instantiation per ring and per number of rounds");
+  static_assert(kSquaresRing == 4, "one instantiation per ring");
   switch (a.n_present) {
-    case 1: return launch_squares_r<1, 1>(a, g, s);
-    case 2: return launch_squares_r<2, 1>(a, g, s);
-    case 3: return launch_squares_r<3, 1>(a, g, s);
-    case 4: return launch_squares_r<4, 1>(a, g, s);
-    case 5: return launch_squares_r<5, 1>(a, g, s);
-    case 6: return launch_squares_r<6, 1>(a, g, s);
-    case 7: return launch_squares_r<7, 1>(a, g, s);
-    case 8: return launch_squares_r<8, 1>(a, g, s);
-    default: break;
-  }
-  switch ((a.n_present + kSquaresRing - 1) / kSquaresRing) {
-    case 2: return launch_squares_r<8, 2>(a, g, s);
-    case 3: return launch_squares_r<8, 3>(a, g, s);
-    case 4: return launch_squares_r<8, 4>(a, g, s);
-    case 5: return launch_squares_r<8, 5>(a, g, s);
-    case 6: return launch_squares_r<8, 6>(a, g, s);
-    case 7: return launch_squares_r<8, 7>(a, g, s);
-    default: return launch_squares_r<8, 8>(a, g, s);
+    case 1: return launch_squares_r<1, false>(a, g, s);
+    case 2: return launch_squares_r<2, false>(a, g, s);
+    case 3: return launch_squares_r<3, false>(a, g, s);
+    case 4: return launch_squares_r<4, false>(a, g, s);
+    default: return launch_squares_r<4, true>(a, g, s);
   }
 }
 

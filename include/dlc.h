@@ -688,7 +688,7 @@ int32_t dlc_expert_weights(const int64_t* counts, int64_t counts_stride, int32_t
 /*
  * dlc_outer_grad_norm -- the global norm of the merged outer gradient over all tensors of
  * the call, and the factor that clips it.  With g as in dlc_merge_outer_step:
- *   norm[0]       = sqrt(sum of g^2)                     (squares summed in fp64, in a fixed order)
+ *   norm[0]       = sqrt(sum of g^2)                     (fp64, in a fixed order)
  *   grad_scale[0] = min(1, max_norm / norm), or 0 where norm is not finite
  *                   (dlc_merge_clipped_step then leaves the step out)
  *   codes, codebook, weights  as dlc_merge_outer_step
@@ -700,11 +700,7 @@ int32_t dlc_expert_weights(const int64_t* counts, int64_t counts_stride, int32_t
  *   norm, grad_scale  device fp64 [1], written
  *   workspace       >= dlc_outer_grad_norm_workspace_bytes(tensors, n_tensors) bytes,
  *                   256-byte aligned, no initial contents required
- * In calls of over a million elements or so an element's g is off by less than
- * K 2^-31 sum_i |w_i| max_c |codebook[i][t][c]| (K present learners), as 32-bit integers
- * stand for the weighted entries, and the norm by far less (2^-34 of itself or so: the
- * roundings differ from block to block and average out); an entry that is not finite then
- * makes the norm not finite whether a code refers to it or not.  No written buffer may overlap another.
+ * No written buffer may overlap another.
  */
 int32_t dlc_outer_grad_norm_workspace_bytes(const dlc_tensor* tensors, int32_t n_tensors, size_t* bytes);
 

@@ -8,10 +8,7 @@ row's largest distance from its maximum that a probability above 2^-126 has, R(D
   * the gradient p (c - sum p c): with A the largest |c|, p A (3 R + 64 u), then the type's rounding, eps / 2 of the
     value or half its smallest subnormal;
   * counts, totals, merge weights and the step: the same operations in the same order: equal;
-  * the norm: fp64 sums in some order, relative 2^-40; and from 256 blocks of two tiles of 4096 elements on, where a
-    learner's entries are integers of unit M / (2^31 - 64), M = sum_i |w_i| max_c |cb_i[c]| over the tensor's
-    learners: a unit at most for each of K, so K M 2^-31 for an element, and by the triangle inequality the root of the
-    sum of these squares for the norm.  The factor is max_norm over it: the same, relatively.
+  * the norm: fp64 sums in some order: relative 2^-40.
 """
 import numpy as np
 import pytest
@@ -346,15 +343,7 @@ class Outer:
                                 max_norm=max_norm, tensor_weights=None if share is None else self.share)
         norm, scale = experts.outer_grad_norm(self.codes.cpu().numpy(), self.codebook.cpu().numpy(), self.weights,
                                               self.tensors, share, max_norm)
-        k = sum(w > 0 for w in self.weights)
-        off = 0.0
-        for t, (_, _, n) in enumerate(self.tensors):
-            w = np.array(self.weights) / sum(self.weights) if share is None else share[t]
-            m = sum(abs(w[i]) * float(self.codebook[i, t].abs().max()) for i in range(self.k) if w[i] != 0)
-            off += n * (k * m * 2.0 ** -31 * (1 + 2.0 ** -20)) ** 2
-        blocks = sum(-(-n // 8192) for _, _, n in self.tensors)
-        tol = 2.0 ** -40 * norm + (off ** 0.5 if blocks >= 256 else 0.0)
-        assert abs(float(self.norm) - norm) <= tol and abs(float(self.scale) - scale) <= 2 * tol / norm * scale + 2.0 ** -52
+        assert abs(float(self.norm) - norm) <= 2.0 ** -40 * norm and abs(float(self.scale) - scale) <= 2.0 ** -40 * scale
         return float(self.scale)
 
     def check_step(self, share, scale):
@@ -367,7 +356,7 @@ class Outer:
         assert np.array_equal(self.theta.cpu().numpy(), th) and np.array_equal(self.mom.cpu().numpy(), mo)
 
 
-LISTS = {"integer_tables": [1 << 21, 3, 500_001, 70_000], "one": [1], "vectors": [4096] * 4, "edges": [63, 64, 65, 4095, 4096, 4097, 8191, 8193, 1, 2],
+LISTS = {"large": [1 << 21, 3, 500_001, 70_000], "one": [1], "vectors": [4096] * 4, "edges": [63, 64, 65, 4095, 4096, 4097, 8191, 8193, 1, 2],
          "ragged": [1, 100003, 65, 64 * 300 + 9, 31, 77777], "many": [(37 * i) % 700 + 1 for i in range(400)]}
 
 
@@ -403,7 +392,7 @@ def test_without_weights_and_factor_it_is_the_outer_step():
     assert torch.equal(th, o.theta) and torch.equal(mo, o.mom)
 
 
-@pytest.mark.parametrize("sizes", [LISTS["edges"], LISTS["ragged"], LISTS["integer_tables"]])
+@pytest.mark.parametrize("sizes", [LISTS["edges"], LISTS["ragged"], LISTS["large"]])
 def test_a_gradient_that_is_not_finite_is_left_out(sizes):
     o = Outer(sizes, 2)
     o.codebook[1, 3, :] = float("inf")
