@@ -39,7 +39,7 @@ constexpr int64_t kSelfCount = 8192;
 // Up to so many sums (blocks times experts) one block a learner does the final ones: above it a single CU's
 // loads take longer than the ticket of several blocks (16384 sums: 20.4 us a call against 18.5).
 constexpr int64_t kOneFinal = 8192;
-constexpr int64_t kMaxStride = int64_t(1) << 48;
+constexpr int64_t kMaxReach = int64_t(1) << 48;  // of a strided array, in elements
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -111,7 +111,11 @@ bool aligned_to(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_
 struct Strided {
   const void* p;
   int64_t learner, token, width, size;
-  bool sound() const { return learner >= 0 && learner <= kMaxStride && token >= 0 && token <= kMaxStride; }
+  // strides that no sum below can overflow with
+  bool sound(int64_t learners, int64_t tokens) const {
+    return learner >= 0 && learner <= kMaxReach / std::max<int64_t>(1, learners) && token >= 0 &&
+           token <= kMaxReach / std::max<int64_t>(1, tokens);
+  }
   bool rows_apart(int64_t learners, int64_t tokens) const {
     const auto nested = [&](int64_t inner, int64_t n_inner, int64_t outer, int64_t n_outer) {
       return (n_inner < 2 || inner >= width) && (n_outer < 2 || outer >= (n_inner - 1) * inner + width);
@@ -187,8 +191,9 @@ int32_t dlc_expert_balance(const void* logits, int32_t logits_type, int64_t logi
     const Strided c{choices, choices_learner_stride, choices_token_stride, n_choices, id_size};
     const Strided g{grad_logits, grad_learner_stride, grad_token_stride, n_experts, size};
     const Strided k{mask, mask_learner_stride, 1, 1, 1};
-    if (!x.sound() || !c.sound() || (mask && !k.sound()) || (grad_logits && !g.sound()))
-      return fail(DLC_ERR_INVALID_ARGUMENT, "strides must be in [0, 2^48]");
+    if (!x.sound(n_learners, n_tokens) || !c.sound(n_learners, n_tokens) || (mask && !k.sound(n_learners, n_tokens)) ||
+        (grad_logits && !g.sound(n_learners, n_tokens)))
+      return fail(DLC_ERR_INVALID_ARGUMENT, "strides must be >= 0 and stay within 2^48 elements");
     if (!aligned_to(logits, size) || !aligned_to(choices, id_size) || !aligned_to(grad_logits, size) ||
         !aligned_to(loss, 4) || !aligned_to(mean_probs, 4) || !aligned8(counts) || !aligned8(totals) ||
         !aligned8(grad_scale))
@@ -197,7 +202,7 @@ int32_t dlc_expert_balance(const void* logits, int32_t logits_type, int64_t logi
       return fail(DLC_ERR_INVALID_ARGUMENT, "rows of grad_logits overlap");
     const Strided n{counts, counts_stride, 0, n_experts, 8}, t{totals, totals_stride, 0, n_experts, 8};
     const bool several = n_learners > 1;
-    if (!n.sound() || (totals && !t.sound()) || (several && counts_stride < n_experts) ||
+    if (!n.sound(n_learners, 1) || (totals && !t.sound(n_learners, 1)) || (several && counts_stride < n_experts) ||
         (several && totals && totals_stride < n_experts))
       return fail(DLC_ERR_INVALID_ARGUMENT, "rows of counts or totals overlap");
     const bool gradient = grad_logits != nullptr && n_tokens > 0;
@@ -287,7 +292,7 @@ int32_t dlc_expert_weights(const int64_t* counts, int64_t counts_stride, int32_t
     if (n_tensors < 1) return fail(DLC_ERR_INVALID_ARGUMENT, "n_tensors must be >= 1");
     if (!aligned8(counts) || !aligned8(tensor_weights))
       return fail(DLC_ERR_ALIGNMENT, "counts and tensor_weights must be 8-byte aligned");
-    if (counts_stride > kMaxStride || (n_learners > 1 && counts_stride < n_experts) || counts_stride < 0)
+    if (counts_stride > kMaxReach / n_learners || (n_learners > 1 && counts_stride < n_experts) || counts_stride < 0)
       return fail(DLC_ERR_INVALID_ARGUMENT, "rows of counts overlap");
     dlc::WeightArgs a;
     std::memset(&a, 0, sizeof(a));

@@ -625,7 +625,7 @@ int32_t dlc_adamw_coded_step(float* theta_learners, const void* grads, int32_t g
  * What the mask leaves out has no influence, whatever it holds.
  *   logits        device, of logits_type (DLC_FLOAT32, DLC_BFLOAT16, DLC_FLOAT16): element
  *                 (i, t, e) at i * logits_learner_stride + t * logits_token_stride + e
- *                 elements; strides >= 0, aligned to its elements
+ *                 elements; strides >= 0 (within 2^48 elements in all), aligned to its elements
  *   choices       device, of choices_type (DLC_INT32, DLC_INT64), element (i, t, j) with its
  *                 own two strides likewise
  *   mask          device uint8, (i, t) at i * mask_learner_stride + t: 0 leaves the token

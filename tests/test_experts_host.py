@@ -42,7 +42,8 @@ def balance(x=F[0], xt=0, xl=800, xs=8, c=F[1], ct=1, cl=200, cs=2, mask=F[2], m
     (dict(flags=1), INVALID), (dict(flags=17), INVALID), (dict(coef=NAN), INVALID), (dict(coef=INF), INVALID),
     (dict(x=None), INVALID), (dict(c=None), INVALID), (dict(loss=None), INVALID), (dict(counts=None), INVALID),
     (dict(present=[0, 0]), QUORUM), (dict(xl=-8), INVALID), (dict(xs=-1), INVALID), (dict(cl=-1), INVALID),
-    (dict(cs=(1 << 48) + 1), INVALID), (dict(ml=-1), INVALID), (dict(gl=-800), INVALID),
+    (dict(cs=(1 << 48) + 1), INVALID), (dict(xs=1 << 47), INVALID), (dict(gl=1 << 62), INVALID), (dict(ns=1 << 62), INVALID),
+    (dict(ts=-8), INVALID), (dict(ml=1 << 60), INVALID), (dict(ml=-1), INVALID), (dict(gl=-800), INVALID),
     (dict(x=F[0] + 2), ALIGN), (dict(x=F[0] + 1, xt=1), ALIGN), (dict(c=F[1] + 4), ALIGN), (dict(c=F[1] + 2, ct=0), ALIGN),
     (dict(g=F[7] + 1), ALIGN), (dict(loss=F[3] + 2), ALIGN), (dict(means=F[5] + 1), ALIGN), (dict(counts=F[4] + 4), ALIGN),
     (dict(totals=F[6] + 4), ALIGN), (dict(up=F[8] + 4), ALIGN), (dict(ws=F[9] + 8), ALIGN),
@@ -94,7 +95,7 @@ def weights(counts=F[0], stride=4, k=2, e=4, w=(1.0, 2.0), q=None, of=(-1, 0, 3)
     (dict(k=0), INVALID), (dict(k=65), INVALID), (dict(counts=None), INVALID), (dict(w=None), INVALID),
     (dict(of=None), INVALID), (dict(out=None), INVALID), (dict(e=0), INVALID), (dict(e=32768, stride=40000), INVALID),
     (dict(n=0), INVALID), (dict(counts=F[0] + 4), ALIGN), (dict(out=F[1] + 4), ALIGN), (dict(stride=3), INVALID),
-    (dict(stride=-4), INVALID), (dict(w=(-1.0, 2.0)), INVALID), (dict(w=(NAN, 2.0)), INVALID), (dict(w=(INF, 2.0)), INVALID),
+    (dict(stride=-4), INVALID), (dict(stride=1 << 60), INVALID), (dict(w=(-1.0, 2.0)), INVALID), (dict(w=(NAN, 2.0)), INVALID), (dict(w=(INF, 2.0)), INVALID),
     (dict(w=(0.0, 0.0)), QUORUM), (dict(q=(-1.0, 1.0)), INVALID), (dict(q=(1.0, NAN)), INVALID), (dict(of=(4,)), INVALID),
     (dict(of=(-2,)), INVALID), (dict(out=F[0] + 8), INVALID), (dict(out=F[0] + 56), INVALID),
 ])
