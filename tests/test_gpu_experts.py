@@ -524,3 +524,62 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for r, w in zip(routers, want):
         assert all(torch.equal(a, b) for a, b in zip((r.loss, r.grad, r.counts), w))
+
+
+def test_rows_further_apart_than_32_bits_count():
+    """Tokens 2^26 elements apart, and a tensor past 2^32 bytes of a row of codes."""
+    t, e, far = 66, 16, 1 << 26
+    near = Router(1, t, e, 2, "bf16", masked=True, seed=11)
+    buf = torch.zeros(t * far, dtype=torch.bfloat16, device=DEV)
+    q = Router(1, t, e, 2, "bf16", masked=True, seed=11)
+    q.x = buf.as_strided((1, t, e), (0, far, 1))
+    q.x.copy_(near.x)
+    out = buf.as_strided((1, t, e), (0, far, 1), storage_offset=64)
+    spare = torch.zeros((1, t, e), dtype=torch.bfloat16, device=DEV)
+    near.call(grad_logits=spare)
+    with pytest.raises(dlc.DlcError, match="overlap"):  # its rows lie between the logits' rows
+        q.call(grad_logits=out)
+    del out
+    q.call(grad_logits=None)
+    assert torch.equal(q.loss, near.loss) and torch.equal(q.counts, near.counts)
+    logits = near.x
+    q.x = logits
+    out = buf.as_strided((1, t, e), (0, far, 1))
+    q.call(grad_logits=out)
+    assert torch.equal(out, spare) and torch.equal(q.loss, near.loss)
+    del buf, out, q
+    stride, n = (1 << 32) + 128 * 64, 5001
+    g = torch.Generator().manual_seed(0)
+    codes = torch.zeros((2, stride), dtype=torch.uint8, device=DEV)
+    lo = stride - 5056
+    codes[:, lo:] = torch.randint(0, 256, (2, 5056), generator=g, dtype=torch.uint8).to(DEV)
+    o = Outer([n], 2, seed=1)
+    far_tensors = [(o.tensors[0][0], lo, n)]
+    _, at, _ = o.tensors[0]
+    o.codes[:, at:at + 5056] = codes[:, lo:]
+    dlc.dlc_outer_grad_norm(o.codes, o.codebook, o.weights, o.tensors, o.norm, o.scale, o.ws, max_norm=1.0)
+    norm, scale = torch.zeros_like(o.norm), torch.zeros_like(o.scale)
+    dlc.dlc_outer_grad_norm(codes, o.codebook, o.weights, far_tensors, norm, scale, o.ws, max_norm=1.0)
+    assert torch.equal(norm, o.norm) and torch.equal(scale, o.scale) and float(norm) > 0
+    th, mo = o.theta.clone(), o.mom.clone()
+    dlc.dlc_merge_clipped_step(o.theta, o.mom, o.codes, o.codebook, o.weights, o.tensors, grad_scale=scale)
+    dlc.dlc_merge_clipped_step(th, mo, codes, o.codebook, o.weights, far_tensors, grad_scale=scale)
+    assert torch.equal(th, o.theta) and torch.equal(mo, o.mom)
+
+
+def test_one_workspace_serves_calls_in_a_row():
+    """Of several sizes and kinds on one stream, without waiting in between."""
+    routers = [Router(2, t, e, 2, kind, seed=t, masked=t % 2 == 0)
+               for t, e, kind in ((6000, 48, "bf16"), (37, 300, "fp32"), (2500, 128, "fp16"), (9000, 8, "bf16"))]
+    ws = max((r.ws for r in routers), key=lambda w: w.numel())
+    for r in routers:
+        r.ws = ws
+    torch.cuda.synchronize()
+    for grad in (True, False):
+        for r in routers:
+            r.args = dict(coef=0.37, mask=r.mask, mean_probs=r.means, grad_scale=r.scale, totals=r.totals,
+                          grad_logits=r.grad if grad else None)
+            r.before = {n: getattr(r, n).clone() for n in ("grad_all", "loss", "means", "counts_all", "totals_all")}
+            dlc.dlc_expert_balance(r.x, r.ids, r.loss, r.counts, r.ws, **r.args)
+        for r in routers:
+            r.check()
