@@ -248,7 +248,8 @@ __device__ __forceinline__ void pass(const BalanceArgs& a, int i, int t0, int t1
 #pragma unroll
       for (int c = 0; c < V; ++c) v[j][c] = (float)raw[j][c];
     }
-    if (__builtin_amdgcn_ballot_w64(live) != ~0ull) {  // what is left out may be no number
+    const bool some = __builtin_amdgcn_ballot_w64(live) != ~0ull;
+    if (some) {  // what is left out may be no number
 #pragma unroll
       for (int j = 0; j < J; ++j) {
 #pragma unroll
@@ -314,6 +315,15 @@ __device__ __forceinline__ void pass(const BalanceArgs& a, int i, int t0, int t1
           v[j][c] *= __fmaf_rn(own[j][c], inv, d);
           if constexpr (MODE == kAccumulate) out[j][c] = live ? (T)((float)old[j][c] + v[j][c]) : old[j][c];
           else out[j][c] = (T)v[j][c];
+        }
+      }
+    }
+    if constexpr (MODE == kGradient) {
+      if (some) {  // its gradient is 0 whatever the factor
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+#pragma unroll
+          for (int c = 0; c < V; ++c) out[j][c] = live ? out[j][c] : (T)0.0f;
         }
       }
     }

@@ -179,6 +179,18 @@ def test_what_the_mask_leaves_out_may_hold_anything(kind, t, e):
 
 
 @pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("factor", [float("inf"), float("nan")])
+@pytest.mark.parametrize("t,e", [(40, 12), (3000, 70), (40, 3)])
+def test_what_the_mask_leaves_out_has_no_gradient_whatever_the_factor(kind, factor, t, e):
+    r = Router(2, t, e, 2, kind, masked=True, seed=4)
+    r.mask[1] = False
+    r.scale.fill_(factor)
+    r.call()
+    assert not r.grad[~r.mask].any() and torch.isfinite(r.loss).all()
+    assert not torch.isfinite(r.grad[0][r.mask[0]]).all()
+
+
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("t,e", [(64, 10), (2500, 48)])
 def test_logits_of_impossible_experts(kind, t, e):
     r = Router(1, t, e, 2, kind, seed=8)
