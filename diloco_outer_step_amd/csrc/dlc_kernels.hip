@@ -1199,7 +1199,10 @@ __global__ __launch_bounds__(kOuterNormThreads) void k_outer_norm_one(const Merg
         for (int e = 0; e < 16; ++e) acc[e] += tab[k * kBuckets + ((q[e / 4] >> (8 * (e % 4))) & 0xffu)];
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sum = __fma_rn(e < n - 16 * tid ? acc[e] : 0.0, acc[e], sum);
+      for (int e = 0; e < 16; ++e) {  // what lies behind the tensor counts for nothing, an infinite entry either
+        const double v = e < n - 16 * tid ? acc[e] : 0.0;
+        sum = __fma_rn(v, v, sum);
+      }
     }
   }
   sum = wave_sum(sum);

@@ -415,6 +415,22 @@ def test_a_gradient_that_is_not_finite_is_left_out(sizes):
     assert torch.equal(th, o.theta) and torch.equal(mo, o.mom)
 
 
+@pytest.mark.parametrize("n", [1, 4095, 5000, 100_001, 2_300_001])
+@pytest.mark.parametrize("k", [2, 6])
+def test_entries_that_no_code_of_the_tensor_names_do_not_count(n, k):
+    """Codes behind a tensor's end, in its last group of 64, name entries that may hold anything."""
+    o = Outer([n, 70], k, seed=n)
+    used = torch.zeros(o.stride, dtype=torch.bool, device=DEV)
+    for _, at, m in o.tensors:
+        used[at:at + m] = True
+    o.codes[:, used] = o.codes[:, used].clamp(max=253)
+    o.codes[:, ~used] = 254
+    o.codes[0, ~used] = 255
+    o.codebook[..., 254] = float("inf")
+    o.codebook[..., 255] = float("nan")
+    o.check_step(None, o.check_norm(None, 0.5))
+
+
 def test_a_gradient_of_zero_has_norm_zero_and_is_not_clipped():
     o = Outer([100, 5000], 2)
     o.codebook.zero_()
