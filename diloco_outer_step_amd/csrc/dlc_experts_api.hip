@@ -302,11 +302,12 @@ int32_t dlc_expert_weights(const int64_t* counts, int64_t counts_stride, int32_t
         return fail(DLC_ERR_INVALID_ARGUMENT, "weights must be finite and >= 0");
       total += weights[i];
       const double w = token_weight ? token_weight[i] : 1.0;
-      if (!(w >= 0.0) || !std::isfinite(w))
-        return fail(DLC_ERR_INVALID_ARGUMENT, "token_weight must be finite and >= 0");
+      if (!(w >= 0.0 && w <= 0x1p900))  // the sum of 64 times 2^63 of them is finite
+        return fail(DLC_ERR_INVALID_ARGUMENT, "token_weight must be in [0, 2^900]");
       a.token_weight[i] = weights[i] > 0.0 ? w : 0.0;
     }
     if (!(total > 0.0)) return fail(DLC_ERR_NO_QUORUM, "all learner weights are zero (no quorum)");
+    if (!std::isfinite(total)) return fail(DLC_ERR_INVALID_ARGUMENT, "the sum of the weights is not finite");
     for (int32_t i = 0; i < n_learners; ++i) a.w_hat[i] = weights[i] / total;
     for (int32_t t = 0; t < n_tensors; ++t) {
       if (expert_of[t] < -1 || expert_of[t] >= n_experts)

@@ -97,6 +97,7 @@ def weights(counts=F[0], stride=4, k=2, e=4, w=(1.0, 2.0), q=None, of=(-1, 0, 3)
     (dict(n=0), INVALID), (dict(counts=F[0] + 4), ALIGN), (dict(out=F[1] + 4), ALIGN), (dict(stride=3), INVALID),
     (dict(stride=-4), INVALID), (dict(stride=1 << 60), INVALID), (dict(w=(-1.0, 2.0)), INVALID), (dict(w=(NAN, 2.0)), INVALID), (dict(w=(INF, 2.0)), INVALID),
     (dict(w=(0.0, 0.0)), QUORUM), (dict(q=(-1.0, 1.0)), INVALID), (dict(q=(1.0, NAN)), INVALID), (dict(of=(4,)), INVALID),
+    (dict(q=(1.0, 1e300)), INVALID), (dict(w=(1.5e308, 1.5e308)), INVALID),
     (dict(of=(-2,)), INVALID), (dict(out=F[0] + 8), INVALID), (dict(out=F[0] + 56), INVALID),
 ])
 def test_the_merge_weights_refuse(bad, code):
