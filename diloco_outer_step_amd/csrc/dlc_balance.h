@@ -33,9 +33,9 @@ __device__ __forceinline__ uint32_t divide(uint32_t f, uint32_t inverse) {
 }
 
 // A learner's choices of tokens [t0, t1) -> hist[0 .. experts), kept tokens -> hist[kCountWords],
-// choices that count for some expert -> hist[kCountWords + 1].  The words of hist hold copies of the histogram, so that lanes with the same choice (routers
-// have favourites, and few experts) add to different words: 16 at most, which are summed
-// at the end.
+// choices that count for some expert -> hist[kCountWords + 1].  The words of hist hold copies of the
+// histogram, so that lanes with the same choice (routers have favourites, and few experts) add to
+// different words: 16 at most, which are summed at the end.
 template <int kThreads, typename I>
 __device__ __forceinline__ void count_choices(const BalanceArgs& a, int i, int t0, int t1, uint32_t* hist) {
   const uint32_t e = (uint32_t)a.experts;
