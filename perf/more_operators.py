@@ -209,7 +209,7 @@ def _prepare_outer(case, s, gen):
         s["momentum"] = torch.empty(stride, device=DEV).normal_(0, 1e-3, generator=gen)
         s["clip"] = 0.25 + 0.75 * torch.rand(1, dtype=torch.float64, device=DEV, generator=gen)
     if s["share"] is not None and case["op"] == "norm":
-        s["share"] = _plain_weights(s).contiguous()  # as the call that makes them writes them
+        s["share"] = _plain_weights(s)
     if own:  # the tensor list as the library reads it, and the norm's workspace
         import diloco_outer_step_amd as dlc
         s["plan"] = dlc.TensorList(tensors)
