@@ -1003,32 +1003,54 @@ def alloc_outer_grad_norm_workspace(tensors, device="cuda") -> torch.Tensor:
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _outer(codes, codebook, weights, tensors, tensor_weights, bufs):
-    """Checks that the merged gradient's calls share -> (K, learner_stride, weights as a C array)."""
+def _dense(t: torch.Tensor, stream) -> torch.Tensor:
+    """t itself if it is contiguous, else a copy of it, made (and given back to torch's allocator) on the call's
+    stream."""
+    if t.is_contiguous():
+        return t
+    if stream is None:
+        stream = torch.cuda.current_stream(t.device)
+    elif not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    elif stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the call's buffers on {t.device}")
+    with torch.cuda.stream(stream):
+        return t.contiguous()
+
+
+def _outer(codes, codebook, weights, tensors, tensor_weights, bufs, stream):
+    """Checks that the merged gradient's calls share -> (K, learner_stride, weights as a C array, dense tensor_weights)."""
     k, stride = _row_shape(codes, tensors, "codes")
     w = _doubles(weights, k, "weights")
     nt = len(tensors)
     if not isinstance(codebook, torch.Tensor):
         raise TypeError(f"codebook must be a torch.Tensor, not {type(codebook).__name__}")
     bufs = [("codes", codes, torch.uint8, (k, stride)), ("codebook", codebook, torch.float32, codebook.shape), *bufs]
-    if tensor_weights is not None:
+    view = isinstance(tensor_weights, torch.Tensor) and not tensor_weights.is_contiguous()
+    if view:  # a dense copy of it will be used: its shape is checked here, type and device by one element
+        if tuple(tensor_weights.shape) != (nt, k):
+            raise ValueError(f"tensor_weights must have shape ({nt}, {k}), not {tuple(tensor_weights.shape)}")
+        bufs.append(("tensor_weights", tensor_weights[:1, 0], torch.float64, (1,)))
+    elif tensor_weights is not None:
         bufs.append(("tensor_weights", tensor_weights, torch.float64, (nt, k)))
     _check_buffers(bufs)
     if codebook.numel() < k * nt * DLC_N_BUCKETS:
         raise ValueError(f"codebook holds {codebook.numel()} elements; the call needs at least {k * nt * DLC_N_BUCKETS}")
-    return k, stride, w
+    return k, stride, w, _dense(tensor_weights, stream) if view else tensor_weights
 
 
 def dlc_outer_grad_norm(codes, codebook, weights, tensors, norm, grad_scale, workspace, max_norm=float("inf"),
                         tensor_weights=None, stream=None):
     """The merged outer gradient's norm over all tensors into norm, and the factor that clips it to
     max_norm into grad_scale (0 where the norm is not finite); both device fp64 [1].
-    tensor_weights: device fp64 [T, K] (dlc_expert_weights) in place of the normalized weights."""
+    tensor_weights: device fp64 [T, K] (dlc_expert_weights) in place of the normalized weights; a view that is not
+    contiguous (a learner-major table's transpose) is copied first, on the call's stream."""
     if not isinstance(workspace, torch.Tensor):
         raise TypeError(f"workspace must be a torch.Tensor, not {type(workspace).__name__}")
-    k, stride, w = _outer(codes, codebook, weights, tensors, tensor_weights,
-                          (("norm", norm, torch.float64, (1,)), ("grad_scale", grad_scale, torch.float64, (1,)),
-                           ("workspace", workspace, torch.uint8, workspace.shape)))
+    k, stride, w, tensor_weights = _outer(
+        codes, codebook, weights, tensors, tensor_weights,
+        (("norm", norm, torch.float64, (1,)), ("grad_scale", grad_scale, torch.float64, (1,)),
+         ("workspace", workspace, torch.uint8, workspace.shape)), stream)
     arr, n = _tensors(tensors)
     _on_device(codes.get_device(), stream, _lib.dlc_outer_grad_norm, codes.data_ptr(), stride, k, codebook.data_ptr(),
                _items(w), _address(tensor_weights), arr, n, float(max_norm), norm.data_ptr(), grad_scale.data_ptr(),
@@ -1039,7 +1061,7 @@ def dlc_merge_clipped_step(theta_g, momentum, codes, codebook, weights, tensors,
                            lr=0.7, beta=0.9, stream=None):
     """dlc_merge_outer_step with the merged gradient times grad_scale (device fp64 [1]; the step is
     left out unless it is finite and positive) and, with tensor_weights, each tensor's own
-    weights."""
+    weights, as dlc_outer_grad_norm takes them."""
     end, _ = _extents(tensors)
     bufs = []
     for name, t in (("theta_g", theta_g), ("momentum", momentum)):
@@ -1050,7 +1072,7 @@ def dlc_merge_clipped_step(theta_g, momentum, codes, codebook, weights, tensors,
         bufs.append((name, t, torch.float32, t.shape))
     if grad_scale is not None:
         bufs.append(("grad_scale", grad_scale, torch.float64, (1,)))
-    k, stride, w = _outer(codes, codebook, weights, tensors, tensor_weights, bufs)
+    k, stride, w, tensor_weights = _outer(codes, codebook, weights, tensors, tensor_weights, bufs, stream)
     arr, n = _tensors(tensors)
     _on_device(codes.get_device(), stream, _lib.dlc_merge_clipped_step, theta_g.data_ptr(), momentum.data_ptr(),
                codes.data_ptr(), stride, k, codebook.data_ptr(), _items(w), _address(tensor_weights),

@@ -1,0 +1,92 @@
+"""The mixture-of-experts calls on the GPU, in the corners that tests/test_gpu_experts.py leaves: same oracle, same
+tolerances."""
+import pytest
+import torch
+
+import diloco_outer_step_amd as dlc
+from tests.test_gpu_experts import DEV, LISTS, Outer
+
+pytestmark = pytest.mark.gpu
+
+
+# --- merge weights that are a view ----------------------------------------------------------------
+
+def views_of(share):
+    """The same [T, K] weights in layouts that are not contiguous."""
+    wide = torch.full((share.shape[0], 2 * share.shape[1] + 1), float("nan"), dtype=torch.float64, device=DEV)
+    wide[:, 1::2] = share
+    return {"learner-major": share.T.contiguous().T, "every other column": wide[:, 1::2]}
+
+
+@pytest.mark.parametrize("name", ["edges", "ragged", "many"])
+@pytest.mark.parametrize("k", [2, 5])
+def test_merge_weights_may_be_any_view(name, k):
+    o = Outer(LISTS[name], k, seed=k)
+    o.shares()
+    args = (o.codes, o.codebook, o.weights, o.tensors)
+    dlc.dlc_outer_grad_norm(*args, o.norm, o.scale, o.ws, max_norm=0.5, tensor_weights=o.share)
+    th, mo = o.theta.clone(), o.mom.clone()
+    dlc.dlc_merge_clipped_step(th, mo, *args, grad_scale=o.scale, tensor_weights=o.share)
+    side = torch.cuda.Stream()
+    for view in views_of(o.share).values():
+        assert not view.is_contiguous()
+        for stream in (None, side, side.cuda_stream, 0):
+            norm, scale = torch.zeros_like(o.norm), torch.zeros_like(o.scale)
+            a, b = o.theta.clone(), o.mom.clone()
+            torch.cuda.synchronize()
+            dlc.dlc_outer_grad_norm(*args, norm, scale, o.ws, max_norm=0.5, tensor_weights=view, stream=stream)
+            dlc.dlc_merge_clipped_step(a, b, *args, grad_scale=scale, tensor_weights=view, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(norm, o.norm) and torch.equal(scale, o.scale)
+            assert torch.equal(a, th) and torch.equal(b, mo)
+
+
+def test_merge_weights_that_are_one_row_for_all_tensors():
+    o = Outer(LISTS["edges"], 3, seed=2)
+    row = torch.tensor(o.weights, dtype=torch.float64, device=DEV)
+    row /= row.sum()
+    o.share.copy_(row.expand_as(o.share))
+    norms = []
+    for share in (o.share, row.expand_as(o.share)):
+        dlc.dlc_outer_grad_norm(o.codes, o.codebook, o.weights, o.tensors, o.norm, o.scale, o.ws, tensor_weights=share)
+        norms.append(o.norm.clone())
+    assert torch.equal(*norms) and float(norms[0]) > 0
+
+
+def test_a_view_of_merge_weights_in_a_graph():
+    """Every replay reads the weights that stand in the view then."""
+    o = Outer(LISTS["ragged"], 4, seed=6)
+    o.shares()
+    first = o.share.clone()
+    view = views_of(first)["learner-major"]
+    args = (o.codes, o.codebook, o.weights, o.tensors)
+    th0, mo0 = o.theta.clone(), o.mom.clone()
+
+    def go():
+        dlc.dlc_outer_grad_norm(*args, o.norm, o.scale, o.ws, max_norm=0.5, tensor_weights=view)
+        dlc.dlc_merge_clipped_step(o.theta, o.mom, *args, grad_scale=o.scale, tensor_weights=view)
+
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        go()
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            go()
+    for factor in (1.0, 0.5, 2.0):
+        view.copy_(first * factor)
+        o.theta.copy_(th0)
+        o.mom.copy_(mo0)
+        go()
+        torch.cuda.synchronize()
+        want = [v.clone() for v in (o.norm, o.scale, o.theta, o.mom)]
+        o.theta.copy_(th0)
+        o.mom.copy_(mo0)
+        o.norm.zero_()
+        o.scale.zero_()
+        noise = torch.randn(1 << 18, device=DEV).mul(3.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.isfinite(noise).all()
+        assert all(torch.equal(x, y) for x, y in zip(want, (o.norm, o.scale, o.theta, o.mom)))
