@@ -872,10 +872,16 @@ __device__ __forceinline__ double rda_unit_weight(const MergeArgs& a, const Laun
   return n2 > 0.0 ? a.w_hat[k] / __builtin_sqrt(n2) : 0.0;
 }
 
-//
 // The clipped step's table holds scale * w * codebook_i[c] with the tensor's own weights w.
 __device__ __forceinline__ double merge_weight(const MergeArgs& a, size_t trow, int k) {
   return a.tensor_w != nullptr ? a.tensor_w[trow * a.n_learners + a.learner[k]] : a.w_hat[k];
+}
+
+// An entry of a learner's table.  A tensor's own weight of 0 leaves the learner out, whatever its codebook holds; any
+// other 0 is a product like the rest, so that entries that are no numbers show in the step (the direction's weight of
+// a learner whose norm is NaN is 0).
+__device__ __forceinline__ double merge_entry(const MergeArgs& a, double w, float cb) {
+  return a.tensor_w != nullptr && w == 0.0 ? 0.0 : w * (double)cb;
 }
 
 template <int NR, bool DIR = false>
@@ -899,7 +905,7 @@ __global__ __launch_bounds__(kMergeBlock) __attribute__((amdgpu_waves_per_eu(4))
     double w;
     if (DIR) w = rda_unit_weight(a, g, trow, k);
     else w = a.coef != nullptr ? a.coef[trow * kp + k] : scale * merge_weight(a, trow, k);
-    tab[i] = w != 0.0 ? w * (double)cb : 0.0;  // a weight of 0 leaves the learner out, whatever its codebook holds
+    tab[i] = merge_entry(a, w, cb);
   }
   __syncthreads();
   double dsum = 0.0;  // DIR: this thread's sum of squared direction values
@@ -1096,7 +1102,7 @@ __global__ __launch_bounds__(kBlock) void k_outer_squares(const MergeArgs a, con
     for (int u = 0; u < RING; ++u) {
       if (k0 + u >= kp) break;
       const double w = merge_weight(a, trow, k0 + u);
-      tab[(k0 + u) * kBuckets + tid] = w != 0.0 ? w * (double)cb[u] : 0.0;
+      tab[(k0 + u) * kBuckets + tid] = merge_entry(a, w, cb[u]);
     }
   }
   __syncthreads();
@@ -1187,7 +1193,7 @@ __global__ __launch_bounds__(kOuterNormThreads) void k_outer_norm_one(const Merg
       for (int k = 0; k < kp; ++k) {
         const double w = merge_weight(a, trow, k);
         const float cb = a.codebook[((size_t)a.learner[k] * g.n_tensors_call + trow) * kBuckets + tid];
-        tab[k * kBuckets + tid] = w != 0.0 ? w * (double)cb : 0.0;
+        tab[k * kBuckets + tid] = merge_entry(a, w, cb);
       }
     }
     __syncthreads();
