@@ -248,8 +248,7 @@ __device__ __forceinline__ void pass(const BalanceArgs& a, int i, int t0, int t1
 #pragma unroll
       for (int c = 0; c < V; ++c) v[j][c] = (float)raw[j][c];
     }
-    const bool some = __builtin_amdgcn_ballot_w64(live) != ~0ull;
-    if (some) {  // what is left out may be no number
+    if (__builtin_amdgcn_ballot_w64(live) != ~0ull) {  // what is left out may be no number
 #pragma unroll
       for (int j = 0; j < J; ++j) {
 #pragma unroll
@@ -313,17 +312,19 @@ __device__ __forceinline__ void pass(const BalanceArgs& a, int i, int t0, int t1
         part[j][c] = __fmaf_rn(v[j][c], inv, part[j][c]);
         if constexpr (MODE != kLossOnly) {
           v[j][c] *= __fmaf_rn(own[j][c], inv, d);
-          if constexpr (MODE == kAccumulate) out[j][c] = live ? (T)((float)old[j][c] + v[j][c]) : old[j][c];
+          if constexpr (MODE == kAccumulate) out[j][c] = s == 0.0f ? old[j][c] : (T)((float)old[j][c] + v[j][c]);
           else out[j][c] = (T)v[j][c];
         }
       }
     }
+    // The sum is 0 where nothing is possible and where the token is left out (and nowhere else: the largest
+    // logit's term is nearly 1): the gradient is 0 whatever the factor.
     if constexpr (MODE == kGradient) {
-      if (some) {  // its gradient is 0 whatever the factor
+      if (__builtin_amdgcn_ballot_w64(s == 0.0f) != 0) {
 #pragma unroll
         for (int j = 0; j < J; ++j) {
 #pragma unroll
-          for (int c = 0; c < V; ++c) out[j][c] = live ? out[j][c] : (T)0.0f;
+          for (int c = 0; c < V; ++c) out[j][c] = s == 0.0f ? (T)0.0f : out[j][c];
         }
       }
     }

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import diloco_outer_step_amd as dlc
-from tests.test_gpu_experts import DEV, LISTS, Outer
+from tests.test_gpu_experts import DEV, LISTS, TYPES, Outer, Router
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,31 @@ def test_a_view_of_merge_weights_in_a_graph():
         torch.cuda.synchronize()
         assert torch.isfinite(noise).all()
         assert all(torch.equal(x, y) for x, y in zip(want, (o.norm, o.scale, o.theta, o.mom)))
+
+
+# --- tokens for which nothing is possible ----------------------------------------------------------
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("factor", [float("inf"), float("nan"), -float("inf"), 1.5])
+@pytest.mark.parametrize("t,e,masked", [(40, 12, False), (41, 3, True), (3000, 70, True), (2501, 300, False), (600, 1000, True)])
+def test_a_token_of_no_possible_expert_has_no_gradient_whatever_the_factor(kind, factor, t, e, masked):
+    """One that the mask keeps, and whose logits are all -infinity: the overflowed loss scale of a step that will be
+    left out must not spoil a gradient that is added to."""
+    for accumulate in (False, True):
+        r = Router(2, t, e, 2, kind, masked=masked, seed=t)
+        none = torch.zeros((2, t), dtype=torch.bool, device=DEV)
+        none[:, ::7] = True
+        none[1, t // 2:] = True
+        r.x.masked_fill_(none[..., None], float("-inf"))
+        r.scale[0] = factor
+        if accumulate:
+            r.grad.copy_(torch.randn(r.grad.shape, device=DEV))
+        before = r.grad.clone()
+        r.call(accumulate=accumulate)
+        left = none if r.mask is None else none | ~r.mask
+        want = before if accumulate else torch.zeros_like(before)
+        assert torch.equal(r.grad[left], want[left])
+        assert torch.isfinite(r.loss).all() and torch.isfinite(r.means).all() and torch.isfinite(r.grad[1]).all()
+        assert bool(torch.isfinite(r.grad[0][~left[0]]).all()) == (factor == 1.5)
+        if factor == 1.5:
+            r.check()
