@@ -79,6 +79,21 @@ BalancePartition balance_partition(int64_t tokens, int32_t experts, int64_t top,
   return p;
 }
 
+// As many blocks as any call of at most so many tokens has, with any number of choices, with and without a gradient.
+// A block's tokens are whole steps, so that fewer tokens can make more blocks: of two learners with 1024 experts, 4211
+// tokens make 351 blocks of 12, 3927 make 491 of 8.  But a block has kMinSteps steps or more, and a learner no more blocks
+// than its share of kBalanceBlocks unless kBlockTokens cuts them short, and likewise those that count.  These bounds do not
+// fall as tokens grow, nor as experts do (a step is shorter then).
+BalancePartition most_blocks(int64_t tokens, int32_t experts, int32_t type, int32_t present) {
+  const int64_t step = dlc::balance_tokens(type, experts, dlc::kBalanceBlock);
+  const int64_t share = std::max<int64_t>(1, kBalanceBlocks / present);
+  BalancePartition p{};
+  p.blocks = std::max({int64_t(1), std::min(share, ceil_div(tokens, kMinSteps * step)), ceil_div(tokens, dlc::kBlockTokens)});
+  const int64_t counting = std::min(kMaxCountBlocks, ceil_div(tokens * DLC_MAX_CHOICES, kCountChoices));
+  p.count_blocks = std::max({p.blocks, counting, ceil_div(tokens, dlc::kCountTokens)});
+  return p;
+}
+
 size_t probs_bytes(const BalancePartition& p, int32_t experts, int32_t present) {
   return round256((size_t)present * p.blocks * experts * sizeof(double));
 }
@@ -138,14 +153,11 @@ int32_t dlc_expert_balance_workspace_bytes(int32_t n_learners, int64_t n_tokens,
     if (!bytes) return fail(DLC_ERR_INVALID_ARGUMENT, "bytes is NULL");
     const int32_t rc = check_sizes(n_learners, n_tokens, n_experts);
     if (rc != DLC_OK) return rc;
-    // any type, number of choices and presence
     size_t most = 0;
     for (int32_t present = 1; present <= n_learners; ++present) {
       for (const int32_t type : {DLC_FLOAT32, DLC_BFLOAT16}) {
-        for (const bool gradient : {false, true}) {
-          const BalancePartition p = balance_partition(n_tokens, n_experts, DLC_MAX_CHOICES, type, present, gradient);
-          most = std::max(most, probs_bytes(p, n_experts, present) + counts_bytes(p, n_experts, present) + loss_bytes(p, present));
-        }
+        const BalancePartition p = most_blocks(n_tokens, n_experts, type, present);
+        most = std::max(most, probs_bytes(p, n_experts, present) + counts_bytes(p, n_experts, present) + loss_bytes(p, present));
       }
     }
     *bytes = most;

@@ -647,7 +647,8 @@ int32_t dlc_adamw_coded_step(float* theta_learners, const void* grads, int32_t g
  *   flags         0, or DLC_ACCUMULATE: grad_logits += (one rounding; tokens that are left
  *                 out keep their values)
  *   workspace     >= dlc_expert_balance_workspace_bytes(n_learners, n_tokens, n_experts)
- *                 bytes, 256-byte aligned, no initial contents required
+ *                 bytes, 256-byte aligned, no initial contents required; what serves
+ *                 these sizes serves every call of no more learners, tokens and experts
  * The probabilities are fp32 (each within 2^-17 of itself for logits within 16 of the row's
  * largest), summed in fp32 over at most 16 tokens and from there on in fp64 in a fixed
  * order: repeated calls agree bit for bit.  No written buffer may overlap another, each

@@ -118,3 +118,15 @@ def test_a_token_of_no_possible_expert_has_no_gradient_whatever_the_factor(kind,
         assert bool(torch.isfinite(r.grad[0][~left[0]]).all()) == (factor == 1.5)
         if factor == 1.5:
             r.check()
+
+
+def test_the_workspace_of_the_longest_batch_serves_a_shorter_one():
+    r = Router(2, 3927, 512, 8, "bf16", seed=3)
+    r.ws = dlc.alloc_expert_balance_workspace(2, 4551, 512, DEV)
+    guard = torch.full((r.ws.numel() + 512,), 255, dtype=torch.uint8, device=DEV)
+    start = -guard.data_ptr() % 256
+    r.ws = guard[start:start + r.ws.numel()]
+    for grad in (None, r.grad):
+        r.call(grad_logits=grad)
+        r.check()
+    assert (guard[start + r.ws.numel():] == 255).all()
