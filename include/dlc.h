@@ -644,8 +644,8 @@ int32_t dlc_adamw_coded_step(float* theta_learners, const void* grads, int32_t g
  *   grad_logits   device, of logits_type, with its own two strides (the rows may not overlap);
  *                 NULL = no gradient, and the logits are then read without waiting for the counts
  *   grad_scale    device fp64 [n_learners], or NULL = 1: the loss scale or the upstream gradient
- *   flags         0, or DLC_ACCUMULATE: grad_logits += (one rounding; tokens that are left
- *                 out keep their values)
+ *   flags         0, or DLC_ACCUMULATE: the gradient is added to grad_logits, in fp32, and the
+ *                 sum rounded to logits_type; tokens that are left out keep their values
  *   workspace     >= dlc_expert_balance_workspace_bytes(n_learners, n_tokens, n_experts)
  *                 bytes, 256-byte aligned, no initial contents required; what serves
  *                 these sizes serves every call of no more learners, tokens and experts

@@ -130,3 +130,22 @@ def test_the_workspace_of_the_longest_batch_serves_a_shorter_one():
         r.call(grad_logits=grad)
         r.check()
     assert (guard[start + r.ws.numel():] == 255).all()
+
+
+# --- the norm's rounds of learners -----------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["large", "ragged", "edges", "many"])
+@pytest.mark.parametrize("k,absent", [(4, ()), (5, ()), (5, (0,)), (8, ()), (9, (3,)), (12, ()), (16, ()), (17, ())])
+def test_norm_and_step_of_whole_and_broken_rounds_of_learners(name, k, absent):
+    """Four learners are an instantiation of their own, more take rounds of four; up to sixteen fit the one block."""
+    o = Outer(LISTS[name], k, seed=k, absent=absent)
+    o.check_norm(None)
+    share = o.shares()
+    o.check_step(share, o.check_norm(share, max_norm=0.5))
+
+
+@pytest.mark.parametrize("k", [1, 4, 16])
+def test_the_norm_of_a_few_tiles_with_any_number_of_learners(k):
+    o = Outer(LISTS["vectors"], k, seed=k)
+    share = o.shares()
+    o.check_step(share, o.check_norm(share, max_norm=0.5))
