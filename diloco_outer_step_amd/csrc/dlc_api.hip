@@ -401,6 +401,11 @@ struct OuterInputs {
   }
 };
 
+// The weights' sum, as merge_weights takes it: one that is not finite would leave every learner out.
+bool finite_sum(const double* weights, int32_t n_learners) {
+  return std::isfinite(std::accumulate(weights, weights + n_learners, 0.0));
+}
+
 int32_t run_broadcast(const float* theta_global, float* theta_learners, int64_t learner_stride, int32_t n_learners,
                       const uint8_t* rows, const dlc_tensor* tensors, int32_t n_tensors, hipStream_t s) {
   dlc::BroadcastArgs a;
@@ -1286,7 +1291,9 @@ int32_t dlc_outer_grad_norm(const uint8_t* codes, int64_t learner_stride, int32_
     if (!(max_norm > 0.0)) return fail(DLC_ERR_INVALID_ARGUMENT, "max_norm must be > 0");
     dlc::MergeArgs a;
     int32_t rc = merge_weights(a, weights, n_learners);
-    if (rc == DLC_OK) rc = check_tensors(tensors, n_tensors, learner_stride, true);
+    if (rc != DLC_OK) return rc;
+    if (!finite_sum(weights, n_learners)) return fail(DLC_ERR_INVALID_ARGUMENT, "the sum of the weights is not finite");
+    rc = check_tensors(tensors, n_tensors, learner_stride, true);
     if (rc != DLC_OK) return rc;
     const Partition p = squares_partition(tensors, n_tensors);
     const size_t need = round256((size_t)p.n_slots * sizeof(double));
@@ -1329,6 +1336,7 @@ int32_t dlc_merge_clipped_step(float* theta_global, float* momentum, const uint8
     dlc::MergeArgs a;
     int32_t rc = prepare_merge(a, theta_global, momentum, codes, learner_stride, n_learners, codebook, weights, lr, beta);
     if (rc != DLC_OK) return rc;
+    if (!finite_sum(weights, n_learners)) return fail(DLC_ERR_INVALID_ARGUMENT, "the sum of the weights is not finite");
     if (!aligned8(tensor_weights) || !aligned8(grad_scale))
       return fail(DLC_ERR_ALIGNMENT, "tensor_weights and grad_scale must be 8-byte aligned");
     rc = check_tensors(tensors, n_tensors, learner_stride, true);

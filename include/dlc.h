@@ -692,7 +692,7 @@ int32_t dlc_expert_weights(const int64_t* counts, int64_t counts_stride, int32_t
  *   norm[0]       = sqrt(sum of g^2)                     (fp64, in a fixed order)
  *   grad_scale[0] = min(1, max_norm / norm), or 0 where norm is not finite
  *                   (dlc_merge_clipped_step then leaves the step out)
- *   codes, codebook, weights  as dlc_merge_outer_step
+ *   codes, codebook, weights  as dlc_merge_outer_step; the sum of the weights finite
  *   tensor_weights  device fp64 [n_tensors][n_learners] (dlc_expert_weights): tensor t
  *                   takes tensor_weights[t][i] in place of w_hat_i, for learners with
  *                   weights[i] > 0; finite, 0 = this learner has no part in this tensor;
@@ -718,7 +718,7 @@ int32_t dlc_outer_grad_norm(const uint8_t* codes, int64_t learner_stride, int32_
  * (fp64).  A factor that is not finite and positive leaves the step out: nothing is
  * written.  A factor from dlc_outer_grad_norm over a whole model serves each of its fragments.
  *   grad_scale      device fp64 [1], or NULL = 1
- *   tensor_weights  as dlc_outer_grad_norm
+ *   weights, tensor_weights  as dlc_outer_grad_norm
  * Other arguments and errors as dlc_merge_outer_step, with which the call agrees bit for bit
  * where both are NULL.  Neither theta_global nor momentum may overlap another buffer.
  */

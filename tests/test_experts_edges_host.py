@@ -9,9 +9,9 @@ import pytest
 import torch
 
 import diloco_outer_step_amd as dlc
-from tests.test_experts_host import L, balance
+from tests.test_experts_host import L, balance, outer_norm, step
 from tests.test_host_sanitizers import CLANG, ROOT, asan_runtime, hostsan_library
-from tests.test_inner_host import WORKSPACE
+from tests.test_inner_host import F, INVALID, WORKSPACE
 
 
 # --- merge weights that are a view ----------------------------------------------------------------
@@ -38,6 +38,13 @@ def test_merge_weights_may_be_a_view_of_the_right_shape_and_type(view, match):
     th = torch.zeros(256)
     with pytest.raises(ValueError, match=f"(codes|tensor_weights).*{match}"):
         dlc.dlc_merge_clipped_step(th, th, a["codes"], a["cb"], [1.0, 1.0], a["tensors"], tensor_weights=view)
+
+
+@pytest.mark.parametrize("tw", [None, F[5]])
+def test_weights_whose_sum_is_not_finite_are_refused(tw):
+    """Each divided by it would be 0: every learner left out, without a word."""
+    for call in (outer_norm, step):
+        assert call(w=(1.5e308, 1.5e308), tw=tw) == INVALID and "sum" in dlc.dlc_last_error()
 
 
 # --- the workspace of the balance loss ---------------------------------------------------------------
