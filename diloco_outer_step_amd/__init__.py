@@ -974,7 +974,7 @@ def _doubles(values, k: int, name: str) -> array.array:
 
 def dlc_expert_weights(counts, weights, expert_of, tensor_weights, token_weight=None, stream=None):
     """Merge weights of every (tensor, learner), device fp64 [T, K], from the experts' counts, device
-    int64 [K, experts]: a tensor of expert expert_of[t] by the tokens that each present learner
+    int64 [K, experts] (32767 columns at most): a tensor of expert expert_of[t] by the tokens that each present learner
     (weights[i] > 0) sent to it, times token_weight[i] (default 1); a tensor of no expert
     (-1), or of one that got no token, by `weights`.  expert_of: ints, or group_ids of them."""
     if not isinstance(counts, torch.Tensor) or counts.dim() != 2:

@@ -676,6 +676,7 @@ int32_t dlc_expert_balance(const void* logits, int32_t logits_type, int64_t logi
  * entries (weights[i] = 0) are 0, and their counts are not read.
  *   counts         device int64 >= 0 (a negative one counts as 0), (i, e) at
  *                  i * counts_stride + e, read only
+ *   n_experts      1..32767: every column of counts, of all layers where they stand side by side
  *   weights        host double [n_learners], as dlc_merge_outer_step's, their sum finite
  *   token_weight   host double [n_learners], each in [0, 2^900], or NULL = 1: what a learner's
  *                  token is worth (a discount for stale learners)
