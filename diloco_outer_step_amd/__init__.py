@@ -1004,13 +1004,10 @@ def alloc_outer_grad_norm_workspace(tensors, device="cuda") -> torch.Tensor:
 
 
 def _dense(t: torch.Tensor, stream) -> torch.Tensor:
-    """t itself if it is contiguous, else a copy of it, made (and given back to torch's allocator) on the call's
-    stream."""
-    if t.is_contiguous():
-        return t
+    """A dense copy of t, made (and given back to torch's allocator) on the call's stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(t.device)
-    elif not isinstance(stream, torch.cuda.Stream):
+        return t.contiguous()
+    if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=t.device)
     elif stream.device != t.device:
         raise ValueError(f"the stream is on {stream.device}, the call's buffers on {t.device}")
