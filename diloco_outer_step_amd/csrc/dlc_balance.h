@@ -440,6 +440,7 @@ __device__ __forceinline__ void write_counts(const BalanceArgs& a, uint32_t* out
 // Bound by memory where there is enough of it: 32768 x 256 x 8 learners in bf16 with the gradient, 268 MB, 52 to 55 us,
 // 5 TB/s (a copy of as much takes 50); 131 vector instructions for a wave's 512 logits, 62% of its time.  Small
 // calls are all latency: 4096 x 64 x 4 learners (4.2 MB) 5 us, of which 2 are the counts' and 1 the final sums'.
+// Added to a gradient, which is read where it is needed: the large one 403 MB, 71 to 80 us, 5 to 5.7 TB/s, the small one 7 us.
 template <typename T, int L, int J, bool NARROW, int MODE>
 __global__ __launch_bounds__(kBalanceBlock) void k_balance(const BalanceArgs a) {
   __shared__ Work<T, kBalanceBlock> work;

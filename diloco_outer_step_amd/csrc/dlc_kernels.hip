@@ -1497,6 +1497,10 @@ hipError_t launch_codebook(const QuantArgs& a, const LaunchGeom& g, hipStream_t 
 // three of them work on faster than what four do: the LDS that they ask for and do not use sees
 // to that.  Clipped step of the 1B set, four blocks against three, us: K = 3 2901, 2870; 4 3092, 2920; 5 3189, 3118;
 // 1 and 2 the same; 6 3216, 3276; 8 3432, 3567.  (Two: 4 2912, 5 3058, but 23.1 against 22.1 on a 4.6M fragment.)
+// Where the lanes of a fragment cycle run other kernels beside a merge, the LDS that it holds is not missed: cycle of the
+// 135M set at K = 4, four blocks against three, us: one lane 2350, 2346, two 1862, 1862, three 1742, 1714, four 1699, 1691
+// (all from graphs; launched directly 2459, 2459, 2501, 2501, 2206, 2208, 2079, 2057), merged by averaged directions on
+// four lanes 1893, 1873; of the edge mix at K = 1 on four 28351, 28186.
 constexpr size_t kFewLearnersLds = 53000;
 constexpr int kFewLearners = 5;
 

@@ -671,8 +671,8 @@ int32_t dlc_expert_balance(const void* logits, int32_t logits_type, int64_t logi
  * counts.  For tensor t of expert e = expert_of[t]:
  *   tensor_weights[t][i] = r_i / sum_j r_j, r_i = token_weight[i] * counts[i][e]  (fp64,
  *                          left-to-right sum, over the learners with weights[i] > 0)
- * and for a tensor of no expert (-1), or of an expert to which no present learner sent a
- * token, weights[i] / sum_j weights[j], as dlc_merge_outer_step weighs it.  Absent learners'
+ * and for a tensor of no expert (-1), or of an expert whose r_i are all 0 (no present learner
+ * sent it a token), weights[i] / sum_j weights[j], as dlc_merge_outer_step weighs it.  Absent learners'
  * entries (weights[i] = 0) are 0, and their counts are not read.
  *   counts         device int64 >= 0 (a negative one counts as 0), (i, e) at
  *                  i * counts_stride + e, read only
